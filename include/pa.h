@@ -1,7 +1,7 @@
 /*
- * pa.h — C ABI of the B200 (sm_100a) paged KV-cache decode library.
+ * pa.h — C ABI of the B200 (sm_100a) paged KV-cache library.
  *
- * Three operations, each enqueued asynchronously on the caller's CUDA stream:
+ * Decode, each operation enqueued asynchronously on the caller's CUDA stream:
  *
  *   pa_decode             paged decode attention: every sequence's one query
  *                         token attends over its KV cache, which is stored in
@@ -9,6 +9,19 @@
  *                         a per-sequence block table.
  *   pa_reshape_and_cache  writes new tokens' K/V rows into their pool slots.
  *   pa_copy_blocks        copy-on-write copies of whole blocks.
+ *
+ * The way of a prompt (or of a step's new tokens) into the cache, in the order
+ * a serving step calls them:
+ *
+ *   pa_assign_slots       block tables, slots and positions of a batch from
+ *                         its requests' lengths, on the device.
+ *   pa_rope_and_cache     rotary positions of q and k; writes the rotated k and
+ *                         v into their pool slots.
+ *   pa_prefill            causal attention over whole prompts, packed one after
+ *                         another, K/V given as packed rows.
+ *   pa_prefill_paged      causal attention of the last tokens of each context
+ *                         over the paged cache (chunked prompts, cached or
+ *                         shared prefixes).
  *
  * Memory layouts (row-major, contiguous, device memory unless stated):
  *   q, out        [num_seqs][num_heads][head_dim]            fp16 or bf16
@@ -82,6 +95,8 @@ typedef enum {
 #define PA_DEVERR_PAIR     8u   /* copy pair id outside [0, num_blocks) */
 #define PA_DEVERR_TIMEOUT 16u   /* a bounded device-side wait ran out */
 #define PA_DEVERR_QRANGE  32u   /* pa_decode_fp8: a bf16 query element above 65504 in magnitude */
+#define PA_DEVERR_BLOCKS  64u   /* pa_assign_slots: more blocks needed than are free */
+#define PA_DEVERR_TOKENS 128u   /* more new tokens than rows, or bad sequence boundaries */
 
 /* Opaque CUDA stream handle (cudaStream_t). */
 typedef void *pa_stream_t;
@@ -397,6 +412,153 @@ PA_API pa_status pa_reshape_and_cache(const void *k, const void *v, void *k_pool
                                const int64_t *slot_mapping, int num_tokens,
                                int num_kv_heads, int head_dim, int block_size,
                                int num_blocks, int dtype, pa_stream_t stream);
+
+/*
+ * Block tables, slots and positions of a step's tokens, from request lengths:
+ * the block manager's allocate, append and free for a whole batch, on the
+ * device and without a host round trip.
+ *
+ * Request s holds context_lens[s] tokens in the first
+ * ceil(context_lens[s] / block_size) blocks of its table row.
+ *   new_lens[s] >= 0  that many tokens are appended (0: nothing changes);
+ *   new_lens[s] <  0  the request ends: its blocks return to the free list.
+ * The free list is a stack: free_blocks[0 .. *num_free) are the free block
+ * ids and the last one is handed out first. Ended requests' blocks are pushed
+ * first, in request order and each in table order; then every request in order
+ * takes the blocks its new tokens need. The result is the host block
+ * manager's free_seq for each ended request followed by allocate / append_slot
+ * for the others.
+ *
+ * Outputs:
+ *   block_tables      new blocks entered at their places; other entries as they were
+ *   free_blocks       entries from *num_free on, as far as the new stack reaches
+ *   context_lens_out  [num_seqs] lengths with the new tokens (0 for ended requests)
+ *   num_free_out      [1] size of the free list
+ *   cu_seqlens        [num_seqs + 1] first new token of each request, packed
+ *   positions         [max_tokens] int32 position of each new token; -1 behind the last
+ *   slot_mapping      [max_tokens] int64 slot of each new token; -1 behind the last
+ * context_lens_out may be context_lens and num_free_out may be num_free. With
+ * separate outputs a repeated call on the same inputs gives the same result.
+ *
+ * Defined by: "别再让GPU内存拖后腿了：vLLM的PagedAttention如何像操作系统一样管理KV Cache",
+ * section 2.1 (the pool, its free list and its out-of-memory error) and
+ * "vLLM架构深度解析：PagedAttention如何实现高吞吐LLM推理", section 按需分配. Blocks
+ * shared by several requests are not counted here: a request whose tail block
+ * is shared copies it first (pa_copy_blocks), and one that holds shared blocks
+ * is not ended here.
+ *
+ * A batch that cannot be served whole is refused whole: block_tables and
+ * free_blocks stay as they were, context_lens_out and num_free_out repeat
+ * their inputs, cu_seqlens is 0 throughout, positions and slots are -1, and
+ * a bit says why: PA_DEVERR_BLOCKS (not enough free blocks, or a free list that
+ * does not fit num_blocks), PA_DEVERR_TOKENS (more than max_tokens new tokens),
+ * PA_DEVERR_CONTEXT (a length below 0 or past its table row). A block id out
+ * of range in a table or in the free list is passed on and flagged
+ * (PA_DEVERR_BLOCK_ID).
+ *
+ * All arrays are device memory: int32, 4-byte aligned, slot_mapping int64,
+ * 8-byte aligned. free_blocks has num_blocks entries. num_seqs <= 8192,
+ * block_size in {16, 32, 64}; max_tokens, num_blocks and the tokens of a table row
+ * are below 2^30 - 1. One launch, no workspace.
+ */
+PA_API pa_status pa_assign_slots(int32_t *block_tables, int32_t *free_blocks, int32_t *context_lens_out,
+                                 int32_t *num_free_out, int64_t *slot_mapping, int32_t *positions,
+                                 int32_t *cu_seqlens, const int32_t *context_lens, const int32_t *num_free,
+                                 const int32_t *new_lens, int num_seqs, int max_blocks_per_seq, int block_size,
+                                 int num_blocks, int max_tokens, pa_stream_t stream);
+
+/*
+ * Rotary positions and the cache write in one pass. For token t at position
+ * p = positions[t] and i < rot_dim / 2, the pair (x, y) of every head of q and
+ * k becomes
+ *   x' = mscale * (x cos a - y sin a),  y' = mscale * (y cos a + x sin a),
+ *   a = p * inv_freq[i],
+ * the pair being elements (i, i + rot_dim / 2) of the head, or (2i, 2i + 1)
+ * with interleaved != 0; elements from rot_dim on are copied. q' goes to q_out,
+ * k' to k_out (if not NULL) and, with v, to the token's pool slot (if the pools
+ * are given): k_pool[slot / block_size][h][slot % block_size] = k'[t][h], v alike.
+ *
+ * The angle is reduced in 64 bits, so far positions lose nothing; the products
+ * are in fp32 and rounded once, to nearest even.
+ *
+ * inv_freq: device array of rot_dim / 2 64-bit floats, radians per position.
+ * Scalings for long contexts are scalings of this table (and of mscale, which
+ * multiplies the rotated part only).
+ * positions: [num_tokens] int32; a negative position skips the token: nothing
+ * of it is read or written (the padding rows of pa_assign_slots).
+ * slot_mapping: [num_tokens] int64; a negative slot skips the token's cache
+ * write, one past the pool too, with PA_DEVERR_SLOT. Non-negative slots are
+ * distinct.
+ * q, k, v: [num_tokens][heads][head_dim], fp16 or bf16, heads and elements
+ * contiguous and q_stride, k_stride, v_stride elements from token to token
+ * (multiples of 8, at least heads * head_dim): views of one fused projection
+ * serve as they are. q_out, k_out: contiguous. q_out may be q and k_out may be
+ * k where those are contiguous; otherwise no output overlaps an input.
+ * k_pool, v_pool, v and slot_mapping are NULL together (then k_out is needed),
+ * or all set. rot_dim: a multiple of 16, at most head_dim. Any num_heads and
+ * num_kv_heads >= 1; head_dim and block_size as pa_decode. 16-byte aligned
+ * tensors, 8-byte aligned inv_freq and slot_mapping.
+ */
+PA_API pa_status pa_rope_and_cache(void *q_out, void *k_out, const void *q, const void *k, const void *v,
+                                   void *k_pool, void *v_pool, const int32_t *positions,
+                                   const int64_t *slot_mapping, const void *inv_freq, int num_tokens, int num_heads,
+                                   int num_kv_heads, int head_dim, int rot_dim, int interleaved, int block_size,
+                                   int num_blocks, int q_stride, int k_stride, int v_stride, float mscale, int dtype,
+                                   pa_stream_t stream);
+
+/*
+ * Causal attention over whole prompts, packed one after another: sequence s
+ * is rows cu_seqlens[s] .. cu_seqlens[s + 1] of q, k and v, and its row i sees
+ * rows 0 .. i:
+ *   out[i][h] = sum_{t <= i} softmax_t(scale * q[i][h] . k[t][h / group]) v[t][h / group].
+ *
+ * Defined by: "别再让GPU内存拖后腿了：vLLM的PagedAttention如何像操作系统一样管理KV Cache",
+ * section 3.1, for every prompt token at once (the m.nxbn.cn VLLM explainer,
+ * section 3.2: prefill computes all prompt tokens in one pass).
+ *
+ * cu_seqlens: [num_seqs + 1] int32 in device memory, not decreasing, within
+ * [0, num_tokens]; other values are clamped and flagged (PA_DEVERR_TOKENS).
+ * Rows outside every sequence are left as they were. A row's result depends on
+ * the rows it sees only: infinities and NaN in later rows, in other sequences
+ * and behind the last one do not reach it.
+ * q, k, v and their strides as in pa_rope_and_cache; out [num_tokens][num_heads]
+ * [head_dim] contiguous, not overlapping an input. Heads, head_dim and
+ * dtype as pa_decode. scale must be finite. No workspace; one launch.
+ */
+PA_API pa_status pa_prefill(void *out, const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                            int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                            int q_stride, int k_stride, int v_stride, float scale, int dtype, pa_stream_t stream);
+
+/*
+ * Causal attention of each sequence's last tokens over its paged cache. The
+ * n = cu_seqlens[s + 1] - cu_seqlens[s] query rows of sequence s are the last n
+ * of its context_lens[s] cached tokens (already written, their own K/V
+ * included), so row i sees the first context_lens[s] - n + i + 1 of them. n may
+ * be the whole context (a prompt), a chunk of it, the part behind a cached or
+ * shared prefix, or 1 (pa_decode is faster for batches of single tokens).
+ * Rows that see nothing (context_lens[s] < n) are zero.
+ *
+ * Pools, block_tables, context_lens and max_context_len as pa_decode (16-bit
+ * cache); q, q_stride, cu_seqlens, out, scale and the treatment of other rows
+ * as pa_prefill. Cache slots past a context are never read into a result.
+ *
+ * Where the rows are too few to fill the device their contexts are split and
+ * the parts merged by the log-sum-exp identity in a second launch.
+ * workspace: device memory of at least pa_prefill_paged_workspace_size(...)
+ * bytes, 256-byte aligned, owned by the caller, contents need no
+ * initialisation; calls that overlap in time use different ones.
+ */
+PA_API pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const void *v_pool,
+                                  const int32_t *block_tables, const int32_t *context_lens,
+                                  const int32_t *cu_seqlens, int num_seqs, int num_tokens, int num_heads,
+                                  int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                                  int num_blocks, int max_context_len, int q_stride, float scale, int dtype,
+                                  void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/* Workspace bytes pa_prefill_paged needs for these sizes on the current device
+ * (0 if the shape is invalid). */
+PA_API size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
+                                              int head_dim, int block_size, int max_context_len);
 
 /*
  * Copy-on-write block copies: for each pair p and each pool i,

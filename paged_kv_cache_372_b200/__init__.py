@@ -23,6 +23,7 @@ PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_DEVICE_CHECK = ra
 PA_F16, PA_BF16 = 0, 1
 PA_KV_E4M3, PA_KV_INT8 = 0, 1
 DEVERR_BLOCK_ID, DEVERR_CONTEXT, DEVERR_SLOT, DEVERR_PAIR, DEVERR_TIMEOUT, DEVERR_QRANGE = 1, 2, 4, 8, 16, 32
+DEVERR_BLOCKS, DEVERR_TOKENS = 64, 128
 
 _DTYPES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
@@ -105,6 +106,16 @@ def lib() -> ctypes.CDLL:
         L.pa_launch_count.argtypes = []
         L.pa_decode_noalloc.restype = _I
         L.pa_decode_noalloc.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P]
+        L.pa_assign_slots.restype = _I
+        L.pa_assign_slots.argtypes = [_P] * 10 + [_I] * 5 + [_P]
+        L.pa_prefill.restype = _I
+        L.pa_prefill.argtypes = [_P] * 5 + [_I] * 8 + [_F, _I, _P]
+        L.pa_prefill_paged.restype = _I
+        L.pa_prefill_paged.argtypes = [_P] * 7 + [_I] * 10 + [_F, _I, _P, _SZ, _P]
+        L.pa_prefill_paged_workspace_size.restype = _SZ
+        L.pa_prefill_paged_workspace_size.argtypes = [_I] * 7
+        L.pa_rope_and_cache.restype = _I
+        L.pa_rope_and_cache.argtypes = [_P] * 10 + [_I] * 11 + [_F, _I, _P]
         _lib = L
     return _lib
 
@@ -558,4 +569,188 @@ def pa_decode_noalloc(out, q, k_pool, v_pool, block_tables, context_lens, scale,
         _cuda(block_tables, "block_tables", torch.int32), _cuda(context_lens, "context_lens", torch.int32),
         B, H, Hkv, D, bs, block_tables.shape[1], NB, int(max_context_len), float(scale), _DTYPES[q.dtype],
         int(partition_size), _stream(stream)))
+    return out
+
+
+def _tensors(*named, device=None) -> torch.device:
+    """Checks (tensor, name, shape or None, dtype) tuples: CUDA, contiguous, one device. Returns that device."""
+    for t, name, shape, dtype in named:
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a CUDA tensor")
+        _cuda(t, name, dtype)
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, other tensors on {device}")
+        device = t.device
+    return device
+
+
+def _stream_of(device, stream) -> int:
+    """The given stream, or the current stream of the tensors' device."""
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+
+
+def _rows(t, name, heads, head_dim, dtype, device) -> int:
+    """Token stride of [T][heads][D] rows whose heads and elements are contiguous (tokens may be further apart)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
+        raise ValueError(f"{name} must be a CUDA tensor [T][{heads}][{head_dim}]")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}: a token's heads and elements must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+def pa_assign_slots(block_tables, free_blocks, context_lens, num_free, new_lens, block_size, slot_mapping, positions,
+                    cu_seqlens, context_lens_out=None, num_free_out=None, stream=None) -> None:
+    """Blocks, slots and positions of a step's tokens, from request lengths (the block manager on the device).
+
+    block_tables int32 [B][W] and free_blocks int32 [NB] are updated in place; num_free int32 [1]; context_lens,
+    new_lens int32 [B] (a negative new length ends the request). Writes slot_mapping int64 [T], positions int32 [T]
+    (-1 behind the last token), cu_seqlens int32 [B + 1], and the new lengths and free count, in place unless
+    context_lens_out / num_free_out are given.
+    """
+    context_lens_out = context_lens if context_lens_out is None else context_lens_out
+    num_free_out = num_free if num_free_out is None else num_free_out
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("block_tables must be [B][W] and free_blocks [NB]")
+    B, W = block_tables.shape
+    T = slot_mapping.numel()
+    i32 = torch.int32
+    dev = _tensors((block_tables, "block_tables", None, i32), (free_blocks, "free_blocks", None, i32),
+                   (context_lens, "context_lens", (B,), i32), (num_free, "num_free", (1,), i32),
+                   (new_lens, "new_lens", (B,), i32), (slot_mapping, "slot_mapping", (T,), torch.int64),
+                   (positions, "positions", (T,), i32), (cu_seqlens, "cu_seqlens", (B + 1,), i32),
+                   (context_lens_out, "context_lens_out", (B,), i32), (num_free_out, "num_free_out", (1,), i32))
+    with torch.cuda.device(dev):
+        _check(lib().pa_assign_slots(
+            block_tables.data_ptr(), free_blocks.data_ptr(), context_lens_out.data_ptr(), num_free_out.data_ptr(),
+            slot_mapping.data_ptr(), positions.data_ptr(), cu_seqlens.data_ptr(), context_lens.data_ptr(),
+            num_free.data_ptr(), new_lens.data_ptr(), B, W, int(block_size), free_blocks.numel(), T,
+            _stream_of(dev, stream)))
+
+
+def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, inv_freq, mscale=1.0,
+                      interleaved=False, k_out=None, stream=None) -> torch.Tensor:
+    """Rotates q and k by their positions; writes the rotated k, and v, into their pool slots in the same pass.
+
+    q [T][H][D], k, v [T][Hkv][D], fp16 or bf16, tokens any stride apart (views of a fused projection); q_out, k_out
+    contiguous (q_out may be q). inv_freq: float64 [rot_dim / 2], radians per position. positions int32 [T] (negative:
+    the token is skipped), slot_mapping int64 [T] (negative: no cache write). Without a cache v, k_pool, v_pool and
+    slot_mapping are None and k_out is needed.
+    """
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T][H][D] and k [T][Hkv][D]")
+    T, H, D = q.shape
+    Hkv = k.shape[1]
+    if q.dtype not in _DTYPES:
+        raise ValueError("q must be fp16 or bf16")
+    dt, dev = q.dtype, q.device
+    cache = [v, k_pool, v_pool, slot_mapping]
+    if any(x is None for x in cache) and not all(x is None for x in cache):
+        raise ValueError("v, k_pool, v_pool and slot_mapping go together")
+    qs, ks = _rows(q, "q", H, D, dt, dev), _rows(k, "k", Hkv, D, dt, dev)
+    if k.shape[0] != T:
+        raise ValueError("q and k differ in tokens")
+    need = [(q_out, "q_out", (T, H, D), dt), (positions, "positions", (T,), torch.int32),
+            (inv_freq, "inv_freq", None, torch.float64)]
+    if k_out is not None:
+        need.append((k_out, "k_out", (T, Hkv, D), dt))
+    vs, NB, bs = 0, 0, 16
+    if v is not None:
+        vs = _rows(v, "v", Hkv, D, dt, dev)
+        if v.shape[0] != T or k_pool.dim() != 4:
+            raise ValueError("v must be [T][Hkv][D] and the pools [NB][Hkv][bs][D]")
+        NB, _, bs, _ = k_pool.shape
+        need += [(k_pool, "k_pool", (NB, Hkv, bs, D), dt), (v_pool, "v_pool", (NB, Hkv, bs, D), dt),
+                 (slot_mapping, "slot_mapping", (T,), torch.int64)]
+    _tensors(*need, device=dev)
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    with torch.cuda.device(dev):
+        _check(lib().pa_rope_and_cache(
+            ptr(q_out), ptr(k_out), ptr(q), ptr(k), ptr(v), ptr(k_pool), ptr(v_pool), ptr(positions),
+            ptr(slot_mapping), ptr(inv_freq), T, H, Hkv, D, 2 * inv_freq.numel(), int(bool(interleaved)), bs, NB, qs, ks,
+            vs, float(mscale), _DTYPES[dt], _stream_of(dev, stream)))
+    return q_out
+
+
+def pa_prefill(out, q, k, v, cu_seqlens, scale, stream=None) -> torch.Tensor:
+    """Causal attention over whole prompts packed one after another: sequence s is rows cu_seqlens[s] ..
+    cu_seqlens[s + 1] (int32 [B + 1]) of q [T][H][D] and k, v [T][Hkv][D] (fp16 or bf16, tokens any stride apart).
+    Writes those rows of out [T][H][D]; other rows stay as they were.
+    """
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T][H][D] and k [T][Hkv][D]")
+    T, H, D = q.shape
+    Hkv = k.shape[1]
+    if q.dtype not in _DTYPES:
+        raise ValueError("q must be fp16 or bf16")
+    qs = _rows(q, "q", H, D, q.dtype, q.device)
+    ks, vs = _rows(k, "k", Hkv, D, q.dtype, q.device), _rows(v, "v", Hkv, D, q.dtype, q.device)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v differ in tokens")
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    _tensors((out, "out", (T, H, D), q.dtype), (cu_seqlens, "cu_seqlens", None, torch.int32), device=q.device)
+    with torch.cuda.device(q.device):
+        _check(lib().pa_prefill(
+            out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T,
+            H, Hkv, D, qs, ks, vs, float(scale), _DTYPES[q.dtype], _stream_of(q.device, stream)))
+    return out
+
+
+def pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
+                                    max_context_len) -> int:
+    n = int(lib().pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
+                                                  max_context_len))
+    if n == 0:
+        raise PagedAttentionError(PA_ERR_INVALID, "unsupported shape")
+    return n
+
+
+def alloc_prefill_workspace(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                            device=None) -> torch.Tensor:
+    """Workspace for pa_prefill_paged."""
+    n = pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
+                                        max_context_len)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_prefill_paged(out, q, k_pool, v_pool, block_tables, context_lens, cu_seqlens, scale, max_context_len,
+                     workspace=None, stream=None) -> torch.Tensor:
+    """Causal attention of each sequence's last tokens over its paged cache: rows cu_seqlens[s] .. cu_seqlens[s + 1]
+    of q [T][H][D] are the last ones of its context_lens[s] cached tokens. Pools, tables and lengths as pa_decode
+    (16-bit cache); writes those rows of out [T][H][D], other rows stay as they were.
+    """
+    if not isinstance(q, torch.Tensor) or not isinstance(k_pool, torch.Tensor) or q.dim() != 3 or k_pool.dim() != 4:
+        raise ValueError("q must be [T][H][D] and the pools [NB][Hkv][bs][D]")
+    T, H, D = q.shape
+    NB, Hkv, bs, _ = k_pool.shape
+    if q.dtype not in _DTYPES:
+        raise ValueError("q must be fp16 or bf16")
+    qs = _rows(q, "q", H, D, q.dtype, q.device)
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise ValueError("block_tables must be [B][W]")
+    B, W = block_tables.shape
+    _tensors((out, "out", (T, H, D), q.dtype), (k_pool, "k_pool", (NB, Hkv, bs, D), q.dtype),
+             (v_pool, "v_pool", (NB, Hkv, bs, D), q.dtype), (block_tables, "block_tables", None, torch.int32),
+             (context_lens, "context_lens", (B,), torch.int32), (cu_seqlens, "cu_seqlens", (B + 1,), torch.int32),
+             device=q.device)
+    with torch.cuda.device(q.device):
+        st = _stream_of(q.device, stream)
+        if workspace is None:
+            workspace = alloc_prefill_workspace(B, T, H, Hkv, D, bs, max_context_len, q.device)
+            if st != torch.cuda.current_stream(q.device).cuda_stream:
+                # Allocated on the current stream, used on another: kept until that one has passed.
+                workspace.record_stream(torch.cuda.ExternalStream(st, device=q.device))
+        else:
+            _tensors((workspace, "workspace", None, None), device=q.device)
+        _check(lib().pa_prefill_paged(
+            out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), cu_seqlens.data_ptr(), B, T, H, Hkv, D, bs, W, NB, int(max_context_len), qs,
+            float(scale), _DTYPES[q.dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
     return out

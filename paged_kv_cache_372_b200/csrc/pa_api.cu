@@ -10,6 +10,7 @@
 #include <string>
 
 #include "pa.h"
+#include "pa_host.h"
 #include "pa_cache.cuh"
 #include "pa_common.cuh"
 #include "pa_decode.cuh"
@@ -91,8 +92,28 @@ __global__ void pa_bounded_wait_probe(unsigned long long limit_ns) {
 
 }  // namespace
 
-// Lets other translation units of the library record pa_last_error() text.
+// What the library's other translation units share (pa_host.h).
 void pa_internal_set_last_error(const char *msg) { g_last_error = msg ? msg : ""; }
+
+void pa_internal_count_launch() { ++g_launches; }
+
+pa_status pa_internal_device(int *dev, int *sms) {
+    DeviceInfo info;
+    const pa_status st = device_info(&info);
+    if (st == PA_OK) {
+        *dev = info.dev;
+        *sms = info.sms;
+    }
+    return st;
+}
+
+pa_status pa_internal_error_word(unsigned int **word) {
+    void *p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, pa::g_device_errors);
+    if (e != cudaSuccess) return cuda_fail(e, "error word address");
+    *word = static_cast<unsigned int *>(p);
+    return PA_OK;
+}
 
 extern "C" {
 

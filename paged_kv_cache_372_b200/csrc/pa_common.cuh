@@ -47,10 +47,14 @@ __device__ __forceinline__ bool count_partition(int *counter, int total, bool co
 constexpr unsigned FULL_MASK = 0xffffffffu;
 
 // Per-device error word. Kernels OR PA_DEVERR_* bits into it instead of
-// faulting on a bad index; pa_device_errors() reads and clears it.
+// faulting on a bad index; pa_device_errors() reads and clears it. It lives in
+// the translation unit of pa_api.cu; kernels of the others (which define
+// PA_ERROR_WORD_ELSEWHERE) get its address as an argument.
+#ifndef PA_ERROR_WORD_ELSEWHERE
 __device__ unsigned int g_device_errors;
 
 __device__ __forceinline__ void raise_error(unsigned bits) { atomicOr(&g_device_errors, bits); }
+#endif
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -16,9 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "pa.h"
-
-// Defined in pa_api.cu: records the text pa_last_error() returns.
-void pa_internal_set_last_error(const char *msg);
+#include "pa_host.h"
 
 namespace {
 

@@ -1,0 +1,137 @@
+// Host side of pa_prefill and pa_prefill_paged (include/pa.h).
+#define PA_ERROR_WORD_ELSEWHERE
+#include "pa_host.h"
+#include "pa_prefill.cuh"
+
+namespace {
+
+using namespace pa_host;
+
+template <int D, typename T, bool PAGED>
+pa_status launch(pa::PrefillParams &p, cudaStream_t stream) {
+    const long long items = (long long)p.num_tokens * p.num_heads;
+    const unsigned grid = (unsigned)((items + pa::ROWS_WARPS - 1) / pa::ROWS_WARPS);
+    pa::pa_prefill_rows_kernel<D, T, PAGED><<<grid, pa::ROWS_WARPS * 32, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, PAGED ? "pa_prefill_paged launch" : "pa_prefill launch");
+    pa_internal_count_launch();
+    return PA_OK;
+}
+
+template <bool PAGED>
+pa_status dispatch(pa::PrefillParams &p, int head_dim, int dtype, cudaStream_t s) {
+    if (head_dim == 128)
+        return dtype == PA_F16 ? launch<128, __half, PAGED>(p, s) : launch<128, __nv_bfloat16, PAGED>(p, s);
+    return dtype == PA_F16 ? launch<64, __half, PAGED>(p, s) : launch<64, __nv_bfloat16, PAGED>(p, s);
+}
+
+bool heads_supported(int num_heads, int num_kv_heads) {
+    if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads) return false;
+    const int g = num_heads / num_kv_heads;
+    return g == 1 || g == 2 || g == 4 || g == 8;
+}
+
+// What both entry points check before anything else.
+pa_status check_common(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim, float scale,
+                       int dtype) {
+    if (num_seqs < 0 || num_tokens < 0) return fail(PA_ERR_INVALID, "negative size argument");
+    if (dtype != PA_F16 && dtype != PA_BF16) return fail(PA_ERR_INVALID, "dtype %d", dtype);
+    if (!heads_supported(num_heads, num_kv_heads))
+        return fail(PA_ERR_UNSUPPORTED, "heads %d/%d (1, 2, 4 or 8 query heads per KV head)", num_heads, num_kv_heads);
+    if (num_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 heads");
+    if (head_dim != 64 && head_dim != 128) return fail(PA_ERR_UNSUPPORTED, "head_dim %d", head_dim);
+    if (num_tokens >= (1 << 27)) return fail(PA_ERR_UNSUPPORTED, "num_tokens must be below 2^27");
+    if (!(scale - scale == 0.f)) return fail(PA_ERR_INVALID, "scale must be finite");
+    return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_prefill(void *out, const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int num_seqs,
+                     int num_tokens, int num_heads, int num_kv_heads, int head_dim, int q_stride, int k_stride,
+                     int v_stride, float scale, int dtype, pa_stream_t stream) {
+    pa_internal_set_last_error("");
+    pa_status st = check_common(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, scale, dtype);
+    if (st != PA_OK) return st;
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !k || !v || !cu_seqlens) return fail(PA_ERR_INVALID, "null pointer");
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(cu_seqlens, 4))
+        return fail(PA_ERR_INVALID, "misaligned pointer (16 B tensors, 4 B cu_seqlens)");
+    const long long q_row = (long long)num_heads * head_dim, kv_row = (long long)num_kv_heads * head_dim;
+    if (q_stride % 8 || k_stride % 8 || v_stride % 8 || q_stride < q_row || k_stride < kv_row || v_stride < kv_row)
+        return fail(PA_ERR_INVALID, "token strides must be multiples of 8 and hold a token's heads");
+    pa::PrefillParams p{};
+    p.out = out;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.cu_seqlens = cu_seqlens;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
+    return dispatch<false>(p, head_dim, dtype, static_cast<cudaStream_t>(stream));
+}
+
+size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                       int block_size, int max_context_len) {
+    if (num_seqs < 0 || num_tokens < 0 || max_context_len < 0 || !heads_supported(num_heads, num_kv_heads) ||
+        num_heads > 65535 || (head_dim != 64 && head_dim != 128) || !block_size_supported(block_size))
+        return 0;
+    return 256;
+}
+
+pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const void *v_pool,
+                           const int32_t *block_tables, const int32_t *context_lens, const int32_t *cu_seqlens,
+                           int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                           int block_size, int max_blocks_per_seq, int num_blocks, int max_context_len, int q_stride,
+                           float scale, int dtype, void *workspace, size_t workspace_bytes, pa_stream_t stream) {
+    pa_internal_set_last_error("");
+    if (max_blocks_per_seq <= 0 || num_blocks <= 0 || max_context_len < 0)
+        return fail(PA_ERR_INVALID, "negative or zero size argument");
+    pa_status st = check_common(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, scale, dtype);
+    if (st != PA_OK) return st;
+    if (!block_size_supported(block_size)) return fail(PA_ERR_UNSUPPORTED, "block_size %d", block_size);
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !k_pool || !v_pool || !block_tables || !context_lens || !cu_seqlens || !workspace)
+        return fail(PA_ERR_INVALID, "null pointer");
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(cu_seqlens, 4) || !aligned(workspace, 256))
+        return fail(PA_ERR_INVALID, "misaligned pointer (16 B tensors, 4 B int arrays, 256 B workspace)");
+    if (q_stride % 8 || q_stride < (long long)num_heads * head_dim)
+        return fail(PA_ERR_INVALID, "the token stride must be a multiple of 8 and hold a token's heads");
+    const size_t need = pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                                        block_size, max_context_len);
+    if (workspace_bytes < need)
+        return fail(PA_ERR_INVALID, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    pa::PrefillParams p{};
+    p.out = out;
+    p.q = q;
+    p.k = k_pool;
+    p.v = v_pool;
+    p.cu_seqlens = cu_seqlens;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    const long long table_tokens = (long long)max_blocks_per_seq * block_size;
+    p.ctx_limit = (int)(table_tokens < max_context_len ? table_tokens : max_context_len);
+    p.q_stride = q_stride;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
+    return dispatch<true>(p, head_dim, dtype, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
