@@ -107,6 +107,13 @@ pa_status pa_internal_device(int *dev, int *sms) {
     return st;
 }
 
+pa_status pa_internal_tensor_map_encoder(void **fn) {
+    PFN_cuTensorMapEncodeTiled enc;
+    const pa_status st = tensor_map_encoder(&enc);
+    if (st == PA_OK) *fn = reinterpret_cast<void *>(enc);
+    return st;
+}
+
 pa_status pa_internal_error_word(unsigned int **word) {
     void *p = nullptr;
     const cudaError_t e = cudaGetSymbolAddress(&p, pa::g_device_errors);

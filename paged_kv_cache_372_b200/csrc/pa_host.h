@@ -18,6 +18,9 @@ void pa_internal_count_launch();
 // The current device's index and number of SMs.
 pa_status pa_internal_device(int *dev, int *sms);
 
+// The driver's cuTensorMapEncodeTiled (a PFN_cuTensorMapEncodeTiled).
+pa_status pa_internal_tensor_map_encoder(void **fn);
+
 // Device address of the current device's error word. Looked up on every call
 // (host side once the module is loaded), so it survives a device reset.
 pa_status pa_internal_error_word(unsigned int **word);

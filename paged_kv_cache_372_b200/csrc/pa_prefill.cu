@@ -1,28 +1,113 @@
 // Host side of pa_prefill and pa_prefill_paged (include/pa.h).
 #define PA_ERROR_WORD_ELSEWHERE
+#include <cudaTypedefs.h>
+#include <float.h>
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
 #include "pa_host.h"
-#include "pa_prefill.cuh"
+#include "pa_prefill_mma.cuh"
 
 namespace {
 
 using namespace pa_host;
 
-template <int D, typename T, bool PAGED>
-pa_status launch(pa::PrefillParams &p, cudaStream_t stream) {
-    const long long items = (long long)p.num_tokens * p.num_heads;
-    const unsigned grid = (unsigned)((items + pa::ROWS_WARPS - 1) / pa::ROWS_WARPS);
-    pa::pa_prefill_rows_kernel<D, T, PAGED><<<grid, pa::ROWS_WARPS * 32, 0, stream>>>(p);
+// Rows [tokens][heads][D] with the given token stride, in boxes of 64 elements x
+// box_heads x box_tokens, 128-byte swizzle.
+pa_status encode_rows(PFN_cuTensorMapEncodeTiled enc, CUtensorMap *map, CUtensorMapDataType type, const void *x, int D,
+                      int heads, int tokens, long long stride, int box_heads, int box_tokens) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, step[3] = {1, 1, 1};
+    const CUresult r = enc(map, type, 3, const_cast<void *>(x), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+// A pool's (block, KV head) chunks, each one box: groups of 8 rows, and in a
+// group one 64-element column of all 8 rows after the other.
+pa_status encode_pool(PFN_cuTensorMapEncodeTiled enc, CUtensorMap *map, CUtensorMapDataType type, const void *x, int D,
+                      int block_size, long long chunks) {
+    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)D / 64, (cuuint64_t)block_size / 8, (cuuint64_t)chunks};
+    const cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16, (cuuint64_t)D * 2 * block_size};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)D / 64, (cuuint32_t)block_size / 8, 1}, step[5] = {1, 1, 1, 1, 1};
+    const CUresult r = enc(map, type, 5, const_cast<void *>(x), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+constexpr int kMaxDevices = 64;
+
+template <int D, typename T, bool PAGED, int NQ>
+pa_status launch(pa::PrefillParams &p, bool negate, cudaStream_t stream) {
+    int dev, sms;
+    pa_status st = pa_internal_device(&dev, &sms);
+    if (st != PA_OK) return st;
+    void *fn;
+    if ((st = pa_internal_tensor_map_encoder(&fn)) != PA_OK) return st;
+    const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled>(fn);
+    const auto type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int group = p.num_heads / p.num_kv_heads;
+    pa::PrefillMaps maps;
+    if ((st = encode_rows(enc, &maps.q, type, p.q, D, p.num_heads, p.num_tokens, p.q_stride, group,
+                          pa::PF_BM / group)) != PA_OK)
+        return st;
+    if (PAGED) {
+        const long long chunks = (long long)p.num_blocks * p.num_kv_heads;
+        if ((st = encode_pool(enc, &maps.k, type, p.k, D, p.block_size, chunks)) != PA_OK) return st;
+        if ((st = encode_pool(enc, &maps.v, type, p.v, D, p.block_size, chunks)) != PA_OK) return st;
+    } else {
+        if ((st = encode_rows(enc, &maps.k, type, p.k, D, p.num_kv_heads, p.num_tokens, p.k_stride, 1, pa::PF_BN)) !=
+            PA_OK)
+            return st;
+        if ((st = encode_rows(enc, &maps.v, type, p.v, D, p.num_kv_heads, p.num_tokens, p.v_stride, 1, pa::PF_BN)) !=
+            PA_OK)
+            return st;
+    }
+    using SH = pa::PrefillShape<D, NQ>;
+    auto kernel = pa::pa_prefill_mma_kernel<D, T, PAGED, NQ>;
+    static std::atomic<bool> done[kMaxDevices];
+    if (!done[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::BYTES);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        done[dev].store(true, std::memory_order_release);
+    }
+    // Every sequence has at most one tile that is not full.
+    const int tokens = NQ * pa::PF_BM / group;
+    const long long grid =
+        (p.num_tokens / tokens + (long long)std::min(p.num_seqs, p.num_tokens)) * p.num_kv_heads;
+    if (grid >= (1ll << 31)) return fail(PA_ERR_UNSUPPORTED, "too many tiles");
+    kernel<<<(unsigned)grid, SH::THREADS, SH::BYTES, stream>>>(p, maps, negate);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, PAGED ? "pa_prefill_paged launch" : "pa_prefill launch");
     pa_internal_count_launch();
     return PA_OK;
 }
 
-template <bool PAGED>
-pa_status dispatch(pa::PrefillParams &p, int head_dim, int dtype, cudaStream_t s) {
+template <bool PAGED, int NQ>
+pa_status dispatch(pa::PrefillParams &p, int head_dim, int dtype, bool negate, cudaStream_t s) {
     if (head_dim == 128)
-        return dtype == PA_F16 ? launch<128, __half, PAGED>(p, s) : launch<128, __nv_bfloat16, PAGED>(p, s);
-    return dtype == PA_F16 ? launch<64, __half, PAGED>(p, s) : launch<64, __nv_bfloat16, PAGED>(p, s);
+        return dtype == PA_F16 ? launch<128, __half, PAGED, NQ>(p, negate, s)
+                               : launch<128, __nv_bfloat16, PAGED, NQ>(p, negate, s);
+    return dtype == PA_F16 ? launch<64, __half, PAGED, NQ>(p, negate, s)
+                           : launch<64, __nv_bfloat16, PAGED, NQ>(p, negate, s);
+}
+
+template <bool PAGED>
+pa_status run(pa::PrefillParams &p, int head_dim, float scale, int dtype, cudaStream_t s) {
+    // A negative scale is a positive one of the negated queries (the matrix
+    // instruction negates them); 0 stands for the least positive one, so that
+    // a masked score of -inf stays -inf.
+    const float a = fabsf(scale) * 1.4426950408889634f;
+    p.scale_log2 = a < FLT_MIN ? FLT_MIN : a;
+    const long long rows = (long long)p.num_tokens * (p.num_heads / p.num_kv_heads);
+    if (rows <= (long long)p.num_seqs * pa::PF_BM) return dispatch<PAGED, 1>(p, head_dim, dtype, scale < 0.f, s);
+    return dispatch<PAGED, 2>(p, head_dim, dtype, scale < 0.f, s);
 }
 
 bool heads_supported(int num_heads, int num_kv_heads) {
@@ -75,9 +160,8 @@ pa_status pa_prefill(void *out, const void *q, const void *k, const void *v, con
     p.q_stride = q_stride;
     p.k_stride = k_stride;
     p.v_stride = v_stride;
-    p.scale_log2 = scale * 1.4426950408889634f;
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
-    return dispatch<false>(p, head_dim, dtype, static_cast<cudaStream_t>(stream));
+    return run<false>(p, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
 }
 
 size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
@@ -129,9 +213,8 @@ pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const v
     const long long table_tokens = (long long)max_blocks_per_seq * block_size;
     p.ctx_limit = (int)(table_tokens < max_context_len ? table_tokens : max_context_len);
     p.q_stride = q_stride;
-    p.scale_log2 = scale * 1.4426950408889634f;
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
-    return dispatch<true>(p, head_dim, dtype, static_cast<cudaStream_t>(stream));
+    return run<true>(p, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

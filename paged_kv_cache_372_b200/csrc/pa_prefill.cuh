@@ -16,7 +16,7 @@ struct PrefillParams {
     int num_seqs, num_tokens, num_heads, num_kv_heads;
     int block_size, max_blocks_per_seq, num_blocks, ctx_limit;  // paged only
     long long q_stride, k_stride, v_stride;                     // elements from token to token
-    float scale_log2;                                           // scale * log2(e)
+    float scale_log2;                                           // |scale| * log2(e), above 0
     unsigned int *errors;
 };
 
@@ -43,10 +43,11 @@ __device__ __forceinline__ SeqRange seq_range(const PrefillParams &p, int s, uns
 
 // One row by one warp: keys a lane each for the scores, head elements a lane
 // each for the values, the running maximum and sum of the softmax in 32 bits.
-// Reads the visible keys and values only. q_smem: D floats of this warp.
+// Reads the visible keys and values only. q_smem: D floats of this warp; negate:
+// the scale is -scale_log2.
 template <int D, typename T, bool PAGED>
-__device__ void attend_row(const PrefillParams &p, int s, int row, int h, int visible, float *q_smem,
-                           unsigned &bad) {
+__device__ __noinline__ void attend_row(const PrefillParams &p, int s, int row, int h, int visible, float *q_smem,
+                           bool negate, unsigned &bad) {
     constexpr int E = D / 32;  // output elements of a lane
     const int lane = threadIdx.x & 31;
     const int kvh = h / (p.num_heads / p.num_kv_heads);
@@ -88,7 +89,7 @@ __device__ void attend_row(const PrefillParams &p, int s, int row, int h, int vi
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dot = fmaf(x[i], q_smem[8 * c + i], dot);
             }
-            z = dot * p.scale_log2;
+            z = (negate ? -dot : dot) * p.scale_log2;
         }
         float mt = z;
 #pragma unroll
@@ -121,35 +122,6 @@ __device__ void attend_row(const PrefillParams &p, int s, int row, int h, int vi
                    lane * (E / 2);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) op[e] = Elem<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-}
-
-constexpr int ROWS_WARPS = 8;
-
-// A warp for each (row, head).
-template <int D, typename T, bool PAGED>
-__global__ void __launch_bounds__(ROWS_WARPS * 32) pa_prefill_rows_kernel(const PrefillParams p) {
-    __shared__ float q_smem[ROWS_WARPS][D];
-    const int warp = threadIdx.x >> 5;
-    const long long item = (long long)blockIdx.x * ROWS_WARPS + warp;
-    unsigned bad = 0;
-    // Every sequence's boundaries and length are looked at, also of those that no row finds.
-    for (long long s = item * 32 + (threadIdx.x & 31); s < p.num_seqs; s += (long long)gridDim.x * ROWS_WARPS * 32)
-        seq_range<PAGED>(p, (int)s, bad);
-    if (item < (long long)p.num_tokens * p.num_heads && p.num_seqs > 0) {
-        const int row = (int)(item / p.num_heads), h = (int)(item % p.num_heads);
-        int lo = 0, hi = p.num_seqs;  // the last sequence that starts at or before the row
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.cu_seqlens[mid] <= row)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const SeqRange r = seq_range<PAGED>(p, lo, bad);
-        if (row >= r.row0 && row < r.row0 + r.n)
-            attend_row<D, T, PAGED>(p, lo, row, h, max(r.keys - r.n + (row - r.row0) + 1, 0), q_smem[warp], bad);
-    }
-    if (bad) atomicOr(p.errors, bad);
 }
 
 }  // namespace pa
