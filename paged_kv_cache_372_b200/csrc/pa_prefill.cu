@@ -43,8 +43,10 @@ pa_status encode_pool(PFN_cuTensorMapEncodeTiled enc, CUtensorMap *map, CUtensor
 
 constexpr int kMaxDevices = 64;
 
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
 template <int D, typename T, bool PAGED, int NQ>
-pa_status launch(pa::PrefillParams &p, bool negate, cudaStream_t stream) {
+pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
     int dev, sms;
     pa_status st = pa_internal_device(&dev, &sms);
     if (st != PA_OK) return st;
@@ -73,41 +75,79 @@ pa_status launch(pa::PrefillParams &p, bool negate, cudaStream_t stream) {
     auto kernel = pa::pa_prefill_mma_kernel<D, T, PAGED, NQ>;
     static std::atomic<bool> done[kMaxDevices];
     if (!done[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::BYTES);
+        cudaFuncAttributes attr;
+        cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+        if (attr.numRegs < SH::REGS_LAUNCH)  // the warps' shares come out of these
+            return fail(PA_ERR_CUDA, "the kernel was built with %d registers a thread, %d needed", attr.numRegs,
+                        SH::REGS_LAUNCH);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::BYTES);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         done[dev].store(true, std::memory_order_release);
     }
     // Every sequence has at most one tile that is not full.
     const int tokens = NQ * pa::PF_BM / group;
     const long long grid =
-        (p.num_tokens / tokens + (long long)std::min(p.num_seqs, p.num_tokens)) * p.num_kv_heads;
+        (p.num_tokens / tokens + (long long)std::min(p.num_seqs, p.num_tokens)) * p.num_kv_heads * max_parts;
     if (grid >= (1ll << 31)) return fail(PA_ERR_UNSUPPORTED, "too many tiles");
-    kernel<<<(unsigned)grid, SH::THREADS, SH::BYTES, stream>>>(p, maps, negate);
-    const cudaError_t e = cudaGetLastError();
+    kernel<<<(unsigned)grid, SH::THREADS, SH::BYTES, stream>>>(p, maps);
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, PAGED ? "pa_prefill_paged launch" : "pa_prefill launch");
     pa_internal_count_launch();
+    if (PAGED && max_parts > 1) {
+        const long long rows = (long long)p.num_tokens * p.num_heads;
+        pa::pa_prefill_join_kernel<D, T><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(e, "pa_prefill_paged launch");
+        pa_internal_count_launch();
+    }
     return PA_OK;
 }
 
 template <bool PAGED, int NQ>
-pa_status dispatch(pa::PrefillParams &p, int head_dim, int dtype, bool negate, cudaStream_t s) {
+pa_status dispatch(pa::PrefillParams &p, int head_dim, int dtype, int max_parts, cudaStream_t s) {
     if (head_dim == 128)
-        return dtype == PA_F16 ? launch<128, __half, PAGED, NQ>(p, negate, s)
-                               : launch<128, __nv_bfloat16, PAGED, NQ>(p, negate, s);
-    return dtype == PA_F16 ? launch<64, __half, PAGED, NQ>(p, negate, s)
-                           : launch<64, __nv_bfloat16, PAGED, NQ>(p, negate, s);
+        return dtype == PA_F16 ? launch<128, __half, PAGED, NQ>(p, max_parts, s)
+                               : launch<128, __nv_bfloat16, PAGED, NQ>(p, max_parts, s);
+    return dtype == PA_F16 ? launch<64, __half, PAGED, NQ>(p, max_parts, s)
+                           : launch<64, __nv_bfloat16, PAGED, NQ>(p, max_parts, s);
+}
+
+// How a call is cut up: tiles of rows of an item, key tiles of a part (0: contexts
+// are not split) and the parts the longest context gives.
+struct Cut {
+    int nq, split_tiles, max_parts;
+};
+
+Cut cut_of(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int max_keys, bool paged, int sms) {
+    Cut c{2, 0, 1};
+    const long long rows = (long long)num_tokens * (num_heads / num_kv_heads);
+    if (rows <= (long long)num_seqs * pa::PF_BM) c.nq = 1;
+    if (!paged) return c;
+    const long long slots = (long long)sms * (c.nq == 1 ? 2 : 1);
+    const long long items =
+        std::max<long long>(std::min(num_seqs, num_tokens), ceil_div(rows, c.nq * pa::PF_BM)) * num_kv_heads;
+    const int tiles = (int)ceil_div(max_keys, pa::PF_BN);
+    if (items < 4 * slots && tiles > 8) {
+        const long long parts = std::min<long long>(ceil_div(4 * slots, items), tiles / 8);
+        c.split_tiles = (int)ceil_div(tiles, parts);
+        c.max_parts = (int)ceil_div(tiles, c.split_tiles);
+        if (c.max_parts == 1) c.split_tiles = 0;
+    }
+    return c;
 }
 
 template <bool PAGED>
-pa_status run(pa::PrefillParams &p, int head_dim, float scale, int dtype, cudaStream_t s) {
+pa_status run(pa::PrefillParams &p, const Cut &cut, int head_dim, float scale, int dtype, cudaStream_t s) {
     // A negative scale is a positive one of the negated queries (the matrix
     // instruction negates them); 0 stands for the least positive one, so that
     // a masked score of -inf stays -inf.
     const float a = fabsf(scale) * 1.4426950408889634f;
     p.scale_log2 = a < FLT_MIN ? FLT_MIN : a;
-    const long long rows = (long long)p.num_tokens * (p.num_heads / p.num_kv_heads);
-    if (rows <= (long long)p.num_seqs * pa::PF_BM) return dispatch<PAGED, 1>(p, head_dim, dtype, scale < 0.f, s);
-    return dispatch<PAGED, 2>(p, head_dim, dtype, scale < 0.f, s);
+    p.negate = scale < 0.f;
+    p.split_tiles = cut.split_tiles;
+    return cut.nq == 1 ? dispatch<PAGED, 1>(p, head_dim, dtype, cut.max_parts, s)
+                       : dispatch<PAGED, 2>(p, head_dim, dtype, cut.max_parts, s);
 }
 
 bool heads_supported(int num_heads, int num_kv_heads) {
@@ -115,6 +155,8 @@ bool heads_supported(int num_heads, int num_kv_heads) {
     const int g = num_heads / num_kv_heads;
     return g == 1 || g == 2 || g == 4 || g == 8;
 }
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // What both entry points check before anything else.
 pa_status check_common(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim, float scale,
@@ -161,15 +203,23 @@ pa_status pa_prefill(void *out, const void *q, const void *k, const void *v, con
     p.k_stride = k_stride;
     p.v_stride = v_stride;
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
-    return run<false>(p, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
+    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, num_tokens, false, 0);
+    return run<false>(p, cut, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
 }
 
 size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
                                        int block_size, int max_context_len) {
     if (num_seqs < 0 || num_tokens < 0 || max_context_len < 0 || !heads_supported(num_heads, num_kv_heads) ||
-        num_heads > 65535 || (head_dim != 64 && head_dim != 128) || !block_size_supported(block_size))
+        num_heads > 65535 || (head_dim != 64 && head_dim != 128) || !block_size_supported(block_size) ||
+        num_tokens >= (1 << 27))
         return 0;
-    return 256;
+    if (num_seqs == 0 || num_tokens == 0) return 256;
+    int dev, sms;
+    if (pa_internal_device(&dev, &sms) != PA_OK) return 0;
+    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, true, sms);
+    if (cut.max_parts == 1) return 256;
+    const size_t rows = (size_t)num_tokens * num_heads * cut.max_parts;
+    return align256(rows * sizeof(float2)) + rows * head_dim * sizeof(float);
 }
 
 pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const void *v_pool,
@@ -214,7 +264,13 @@ pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const v
     p.ctx_limit = (int)(table_tokens < max_context_len ? table_tokens : max_context_len);
     p.q_stride = q_stride;
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
-    return run<true>(p, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
+    int dev, sms;
+    if ((st = pa_internal_device(&dev, &sms)) != PA_OK) return st;
+    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, true, sms);
+    const size_t rows = (size_t)num_tokens * num_heads * cut.max_parts;
+    p.part_ml = static_cast<float2 *>(workspace);
+    p.part_acc = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align256(rows * sizeof(float2)));
+    return run<true>(p, cut, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,6 +1,5 @@
-// Device side shared by the prompt attention kernels (pa_prefill,
-// pa_prefill_paged; include/pa.h): parameters, the rows of a sequence and the
-// plain row-at-a-time form.
+// Device side of the prompt attention (pa_prefill, pa_prefill_paged;
+// include/pa.h): parameters, the rows of a sequence and the row-at-a-time form.
 #pragma once
 
 #include "pa_common.cuh"
@@ -17,6 +16,10 @@ struct PrefillParams {
     int block_size, max_blocks_per_seq, num_blocks, ctx_limit;  // paged only
     long long q_stride, k_stride, v_stride;                     // elements from token to token
     float scale_log2;                                           // |scale| * log2(e), above 0
+    bool negate;                                                // the scale is -scale_log2
+    int split_tiles;   // key tiles of a part of a context (paged), 0: contexts are not split
+    float *part_acc;   // [part][token][head][head_dim]: weighted values of the parts
+    float2 *part_ml;   // [part][token][head]: what they are relative to (log2), sum of the weights
     unsigned int *errors;
 };
 
@@ -41,87 +44,102 @@ __device__ __forceinline__ SeqRange seq_range(const PrefillParams &p, int s, uns
     return r;
 }
 
-// One row by one warp: keys a lane each for the scores, head elements a lane
-// each for the values, the running maximum and sum of the softmax in 32 bits.
-// Reads the visible keys and values only. q_smem: D floats of this warp; negate:
-// the scale is -scale_log2.
+// What a row has from a range of keys: weighted values relative to the maximum
+// m (log2 units) and the sum of the weights; D / 32 elements a lane.
+template <int D>
+struct RowPart {
+    float acc[D / 32], m, l;
+};
+
+// One row over the keys [lo, hi), all visible to it, by one warp: a key a lane
+// for the scores, D / 32 elements a lane for the values, the running maximum
+// and sum of the softmax in 32 bits. Reads no other key or value.
 template <int D, typename T, bool PAGED>
-__device__ __noinline__ void attend_row(const PrefillParams &p, int s, int row, int h, int visible, float *q_smem,
-                           bool negate, unsigned &bad) {
-    constexpr int E = D / 32;  // output elements of a lane
+__device__ __noinline__ RowPart<D> attend_row(const PrefillParams &p, int s, int row0, int row, int h, int lo, int hi) {
+    constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const int kvh = h / (p.num_heads / p.num_kv_heads);
-    const int row0 = PAGED ? 0 : p.cu_seqlens[s];
     auto base = [&](const void *x, long long stride, int j) {
         if constexpr (PAGED) {
             int id = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / p.block_size];
-            if ((unsigned)id >= (unsigned)p.num_blocks) {
-                bad |= PA_DEVERR_BLOCK_ID;
-                id = 0;
-            }
+            if ((unsigned)id >= (unsigned)p.num_blocks) id = 0;  // flagged where the tile was loaded
             return static_cast<const T *>(x) +
                    (((size_t)id * p.num_kv_heads + kvh) * p.block_size + j % p.block_size) * D;
         } else {
             return static_cast<const T *>(x) + (size_t)(row0 + j) * stride + (size_t)kvh * D;
         }
     };
-    const T *qp = static_cast<const T *>(p.q) + (size_t)row * p.q_stride + (size_t)h * D;
-    __syncwarp();
-    for (int i = lane; i < D / 2; i += 32) {
-        const float2 x = Elem<T>::pair(reinterpret_cast<const uint32_t *>(qp)[i]);
-        q_smem[2 * i] = x.x;
-        q_smem[2 * i + 1] = x.y;
+    const uint32_t *qp =
+        reinterpret_cast<const uint32_t *>(static_cast<const T *>(p.q) + (size_t)row * p.q_stride + (size_t)h * D);
+    float q[E];  // elements lane * E ..
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+        const float2 x = Elem<T>::pair(qp[lane * (E / 2) + e]);
+        q[2 * e] = p.negate ? -x.x : x.x;
+        q[2 * e + 1] = p.negate ? -x.y : x.y;
     }
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, acc[E];
+    RowPart<D> r;
+    r.m = -INFINITY;
+    r.l = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int j0 = 0; j0 < visible; j0 += 32) {
-        const int count = min(32, visible - j0);
-        float z = -INFINITY;
-        if (lane < count) {
-            const uint4 *kp = reinterpret_cast<const uint4 *>(base(p.k, p.k_stride, j0 + lane));
-            float dot = 0.f;
+    for (int e = 0; e < E; ++e) r.acc[e] = 0.f;
+    for (int j0 = lo; j0 < hi; j0 += 32) {
+        const int count = min(32, hi - j0);
+        const uint4 *kp = reinterpret_cast<const uint4 *>(base(p.k, p.k_stride, j0 + min(lane, count - 1)));
+        float dot = 0.f;
+        for (int c = 0; c < D / 8; ++c) {
+            float x[8];
+            unpack8<T>(kp[c], x);
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                float x[8];
-                unpack8<T>(kp[c], x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dot = fmaf(x[i], q_smem[8 * c + i], dot);
-            }
-            z = (negate ? -dot : dot) * p.scale_log2;
+            for (int i = 0; i < 8; ++i) dot = fmaf(x[i], __shfl_sync(FULL_MASK, q[i % E], c * 8 / E + i / E), dot);
         }
+        const float z = lane < count ? dot * p.scale_log2 : -INFINITY;
         float mt = z;
 #pragma unroll
         for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, o));
-        const float m_new = fmaxf(m, mt);
+        const float m_new = fmaxf(r.m, mt);
         const float ref = m_new == -INFINITY ? 0.f : m_new;  // nothing above -inf yet
-        const float f = exp2f(m - ref);
+        const float f = exp2f(r.m - ref);
         const float w = lane < count ? exp2f(z - ref) : 0.f;
-        m = m_new;
+        r.m = m_new;
         float sum = w;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-        l = l * f + sum;
+        r.l = r.l * f + sum;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= f;
+        for (int e = 0; e < E; ++e) r.acc[e] *= f;
         for (int c = 0; c < count; ++c) {
             const float wc = __shfl_sync(FULL_MASK, w, c);
             const uint32_t *vp = reinterpret_cast<const uint32_t *>(base(p.v, p.v_stride, j0 + c)) + lane * (E / 2);
 #pragma unroll
             for (int e = 0; e < E / 2; ++e) {
                 const float2 x = Elem<T>::pair(vp[e]);
-                acc[2 * e] = fmaf(wc, x.x, acc[2 * e]);
-                acc[2 * e + 1] = fmaf(wc, x.y, acc[2 * e + 1]);
+                r.acc[2 * e] = fmaf(wc, x.x, r.acc[2 * e]);
+                r.acc[2 * e + 1] = fmaf(wc, x.y, r.acc[2 * e + 1]);
             }
         }
     }
-    // A row that sees nothing is zero; one whose scores are all -inf is 0 / 0.
-    const float inv = visible > 0 ? 1.f / l : 0.f;
-    uint32_t *op = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + ((size_t)row * p.num_heads + h) * D) +
-                   lane * (E / 2);
+    return r;
+}
+
+// Stores what a warp has of a row: the output, or a part of a split context.
+template <int D, typename T>
+__device__ __forceinline__ void store_row(const PrefillParams &p, int row, int h, int part, int parts,
+                                          const RowPart<D> &r) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    size_t at = (size_t)row * p.num_heads + h;
+    if (parts > 1) {
+        at += (size_t)part * p.num_tokens * p.num_heads;
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) op[e] = Elem<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        for (int e = 0; e < E; ++e) p.part_acc[at * D + lane * E + e] = r.acc[e];
+        if (lane == 0) p.part_ml[at] = make_float2(r.m, r.l);
+    } else {
+        const float inv = 1.f / r.l;  // scores that are all -inf give 0 / 0
+        uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at * D) + lane * (E / 2);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) out[e] = Elem<T>::pack(r.acc[2 * e] * inv, r.acc[2 * e + 1] * inv);
+    }
 }
 
 }  // namespace pa

@@ -1,11 +1,11 @@
 // Tensor-core kernel of pa_prefill and pa_prefill_paged (include/pa.h).
 //
-// A CTA takes NQ tiles of 128 query rows of one (sequence, KV head) and walks
-// the keys they see in tiles of 128. The rows are (token, query head) pairs of
-// the group, head fastest: all query heads of a KV head share its key and value
+// A work item is NQ tiles of 128 query rows of one (sequence, KV head), walked
+// over the keys they see in tiles of 128. The rows are (token, query head) pairs
+// of the group, head fastest: all query heads of a KV head share its key and value
 // tiles, and a tile spans few tokens, so little of it is masked. For each tile
 //   S = Q K^T      tcgen05.mma, both operands in shared memory, S in TMEM
-//   P = exp2(S * scale_log2 - m)   a thread for each row, registers; P rounded
+//   P = exp2(S * scale_log2 - m)   a thread for each row, in registers; P rounded
 //                  to the input type goes back to TMEM over S
 //   O += P V       tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
 // m is a running maximum of the row and l the running sum, both 32 bits; O and
@@ -13,10 +13,15 @@
 // below 2^8, far inside fp16's range), which after the first tiles is rare.
 //
 // Warps: four softmax warps for each tile of rows, one that issues the copies
-// (TMA) and one that issues the matrix instructions. While the softmax of one
-// tile of rows runs, the other tile's products do. A tile of rows is bound by
-// two things at once at head size 128: 128 x 128 exponentials at 16 a clock and
-// 4 x 128^3 product operations at 8192 a clock, 1024 clocks either way.
+// (TMA), one for each tile of rows that issues its matrix instructions, and one
+// that finds the next work item. While the softmax of one tile of rows runs, the
+// other's products do: at head size 128 a tile needs 128 x 128 exponentials at
+// 16 a clock and 4 x 128^3 product operations at 8192 a clock, 1024 clocks
+// either way, so a quarter of the exponentials go to the FMA units (ex2_fma).
+//
+// CTAs are persistent: a CTA that works on an item takes over the launch of the
+// next one that has not started (clusterlaunchcontrol) and its copies and first
+// product run ahead of the item's end. Items come longest first.
 //
 // Masked places: S is replaced by -inf there (a selection, so NaN and
 // infinities in masked keys do not spread) and P is 0. A NaN or infinity in a
@@ -27,28 +32,41 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "pa_prefill.cuh"
 
 namespace pa {
 
 constexpr int PF_BM = 128;  // rows of a tile
 constexpr int PF_BN = 128;  // keys of a tile
-constexpr uint64_t PF_WAIT_NS = 1000000000ull;
+constexpr int PF_POLY = 4;  // of 16 pairs of exponentials, those on the FMA units
+constexpr uint64_t PF_WAIT_NS = 4000000000ull;
 
 template <int D, int NQ>
 struct PrefillShape {
-    static constexpr int HALVES = D / 64;            // 128-byte columns of a row
-    static constexpr int TILE = 128 * D * 2;         // bytes of a tile of rows (queries, keys or values)
-    static constexpr int THREADS = NQ * 128 + 128;
+    static constexpr int HALVES = D / 64;     // 128-byte columns of a row
+    static constexpr int TILE = 128 * D * 2;  // bytes of a tile of rows (queries, keys or values)
+    static constexpr int SOFTMAX_WARPS = NQ * 4;
+    static constexpr int COPY_WARP = SOFTMAX_WARPS, MMA_WARP = COPY_WARP + 1, PLAN_WARP = COPY_WARP + 3;
+    static constexpr int THREADS = SOFTMAX_WARPS * 32 + 128;
     // NQ = 2: one CTA an SM; NQ = 1: two.
     static constexpr int STAGES = NQ == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 5);
+    // Registers move from the other warps to the softmax warps:
+    // 384 threads x 168 = 256 x 216 + 128 x 72, 256 threads x 128 = 128 x 200 + 128 x 56.
+    static constexpr int REGS_LAUNCH = NQ == 2 ? 168 : 128;
+    static constexpr int REGS_SOFTMAX = NQ == 2 ? 216 : 200, REGS_OTHER = NQ == 2 ? 72 : 56;
+    static_assert(SOFTMAX_WARPS * 32 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * REGS_LAUNCH,
+                  "more registers than launched");
     static constexpr int TMEM_COLS = NQ == 2 ? 512 : 256;
     static constexpr int S_COL = 0, O_COL = NQ * 128;
     static constexpr int OFF_KV = NQ * TILE;
-    static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
-    static constexpr int NUM_BARS = 2 * STAGES + 1 + 3 * NQ;
-    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;        // TMEM address, scratch of locate_tile
-    static constexpr int BYTES = OFF_MISC + 8 + 2 * 16 * 4 + 8 * 4 + 1024;  // and slack for the 1024-byte alignment
+    static constexpr int OFF_NEXT = OFF_KV + STAGES * TILE;  // 16 bytes: the launch taken over
+    static constexpr int OFF_ITEM = OFF_NEXT + 16;           // the work item, 8 integers
+    static constexpr int OFF_TMEM = OFF_ITEM + 32;           // TMEM address
+    static constexpr int OFF_BAR = OFF_TMEM + 16;
+    static constexpr int NUM_BARS = 2 * STAGES + 3 + 6 * NQ;
+    static constexpr int BYTES = OFF_BAR + NUM_BARS * 8 + 1024;  // and slack for the alignment to 1024
 };
 
 // ---- tcgen05 ------------------------------------------------------------------------------------------
@@ -56,24 +74,48 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// The matrix instructions and their commits are issued by the one thread whose
+// `one` is set; the whole warp runs the code around them, so that descriptors
+// and addresses stay in uniform registers. (Issued under a branch of one lane,
+// 8 instructions took 650 to 970 clocks to issue, more than they run.)
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
 }
 
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(one)
+        : "memory");
+}
+
+// Shared-memory matrix descriptor with the 128-byte swizzle: start address and
+// leading byte offset in the low word, stride byte offset, version 1 (bit 46)
+// and swizzle (bit 61) in the high word, all in units of 16 bytes.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return addr >> 4 | (lbo >> 4) << 16; }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return sbo >> 4 | 1u << 14 | 2u << 29; }
+
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t add, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\tsetp.ne.u32 e, %7, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(add), "r"(one)
         : "memory");
 }
 
 // A from TMEM.
-__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                          uint32_t add, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 e, %6, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(add), "r"(one)
         : "memory");
 }
 
@@ -91,13 +133,18 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, float *x) {
         : "r"(addr));
 }
 
-// Waits for the loads issued before and ties their registers to the wait, so
-// that nothing that uses them is moved above it.
+// Ties loaded registers to the wait before: nothing that uses them moves above it.
+template <int N>
+__device__ __forceinline__ void tc_pin(float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(x[i]));
+}
+
+// Waits for the loads issued before, x among them.
 template <int N>
 __device__ __forceinline__ void tc_landed(float (&x)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(x[i]));
+    tc_pin(x);
 }
 
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r) {
@@ -112,11 +159,13 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r) {
         : "memory");
 }
 
-// Shared-memory matrix descriptor with the 128-byte swizzle: start address,
-// leading and stride byte offsets in 16-byte units, version 1 (bit 46).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)((lbo >> 4) & 0x3fff) << 16 |
-           (uint64_t)((sbo >> 4) & 0x3fff) << 32 | 1ull << 46 | 2ull << 61;
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 
 // ---- tensor-map copies --------------------------------------------------------------------------------
@@ -143,6 +192,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;"
@@ -160,100 +215,180 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return *reinterpret_cast<float2 *>(&r);
 }
 
-// ---- which tile a CTA takes ---------------------------------------------------------------------------
-// Tiles are handed out from the longest to the shortest: a tile's level is its
-// position in the context in units of TM tokens, C(d) = number of tiles at
-// level d or above, and tile k has the level d with C(d + 1) <= k < C(d). Every
-// thread of the CTA takes part.
-struct TileAt {
-    int s, tok0;  // sequence, first token of the tile among its rows
-    SeqRange r;
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// 2^x without the special-function unit: x = n + f with n the nearest integer
+// (adding 1.5 x 2^23 leaves it in the low bits), 2^f by a polynomial and n added
+// to the exponent. The coefficients minimise the largest relative error on
+// [-1/2, 1/2] with the constant term 1 (a linear programme over 4001 points):
+// 1.0e-4 of degree 3 for bf16, whose weights are rounded to 2^-9, 2.9e-6 of degree
+// 4 for fp16. x below -127 counts as -127, whose f is 0 and whose result is 0.
+// x up to 127; a NaN gives a weight so large that the row's sums overflow.
+template <typename T>
+__device__ __forceinline__ float2 ex2_fma(float2 x) {
+    x.x = max_nan(x.x, -127.f);
+    x.y = max_nan(x.y, -127.f);
+    const float2 big = make_float2(12582912.f, 12582912.f), less = make_float2(-12582912.f, -12582912.f);
+    const float2 r = add2(x, big);
+    const float2 f = fma2(add2(r, less), make_float2(-1.f, -1.f), x);
+    float2 y;
+    auto c = [](float v) { return make_float2(v, v); };
+    if constexpr (std::is_same<T, __half>::value) {
+        y = fma2(f, c(0.009582576f), c(0.055906828f));
+        y = fma2(f, y, c(0.24024107f));
+        y = fma2(f, y, c(0.6931241f));
+    } else {
+        y = fma2(f, c(0.05500906f), c(0.24221097f));
+        y = fma2(f, y, c(0.6932829f));
+    }
+    y = fma2(f, y, c(1.f));
+    y.x = __int_as_float(__float_as_int(y.x) + (__float_as_int(r.x) << 23));
+    y.y = __int_as_float(__float_as_int(y.y) + (__float_as_int(r.y) << 23));
+    return y;
+}
+
+// ---- work items ---------------------------------------------------------------------------------------
+struct Item {
+    int s, tok0;            // sequence, first token of the tile among its rows
+    int row0, n, keys;      // as SeqRange
+    int part, parts, kvh;   // part of the context and their number, KV head
 };
 
-template <bool PAGED, int NT>
-__device__ bool locate_tile(const PrefillParams &p, int k, int TM, int *scratch, int *found, TileAt &tile,
-                            unsigned &bad) {
-    constexpr int NW = NT / 32;
-    const int tid = threadIdx.x, warp = tid >> 5, B = p.num_seqs;
-    auto level = [&](int s, int &base, int &count) {
+// Key tiles an item walks, [j0, j1), and those of its tiles of rows among them.
+template <int NQ>
+struct Walk {
+    int first;            // row i of the sequence sees the keys below first + i + 1
+    int j0, j1, kv_end;   // kv_end: the keys that any of the rows sees
+    int count[NQ];
+};
+
+template <int NQ>
+__device__ __forceinline__ Walk<NQ> walk_of(const Item &it, int tm, int split_tiles) {
+    Walk<NQ> w;
+    w.first = it.keys - it.n;
+    w.kv_end = 0;
+    int tiles[NQ];
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+        const int a = it.tok0 + t * tm, b = min(it.n, a + tm);
+        const int end = a < b ? max(w.first + b, 0) : 0;
+        tiles[t] = (end + PF_BN - 1) / PF_BN;
+        w.kv_end = max(w.kv_end, end);
+    }
+    const int all = (w.kv_end + PF_BN - 1) / PF_BN;
+    w.j0 = it.parts > 1 ? min(it.part * split_tiles, all) : 0;
+    w.j1 = it.parts > 1 ? min(w.j0 + split_tiles, all) : all;
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) w.count[t] = max(min(tiles[t], w.j1) - w.j0, 0);
+    return w;
+}
+
+// Parts that the context of a sequence is split into.
+__device__ __forceinline__ int parts_of(int keys, int split_tiles) {
+    return split_tiles > 0 ? max((keys + split_tiles * PF_BN - 1) / (split_tiles * PF_BN), 1) : 1;
+}
+
+// Items are handed out from the longest to the shortest, roughly: a tile's
+// position in its context counts in units of TM tokens, positions 0 to 7 are
+// levels of their own and then 8 of them make one, and the items of a level
+// come sequence by sequence and head by head, so that the tiles that walk the
+// same keys run at the same time and share them in L2. (Heads first: a piece of
+// 512 tokens over 32768 read its keys from memory 3 times.) Where contexts are
+// split, parts are about equally long and there is one level. With C(d) the
+// number of tiles of level d or above, item k has the level d with
+// C(d + 1) <= k / heads < C(d). One warp; its calls come with growing k.
+template <bool PAGED>
+struct Finder {
+    int level = -1, above = 0;  // C(level) = above <= the last k / heads
+
+    __device__ __forceinline__ static int start(int d) { return d < 8 ? d : 8 * (d - 7); }
+    __device__ __forceinline__ static int level_of(int position) { return position < 8 ? position : 7 + position / 8; }
+
+    __device__ __forceinline__ static void tiles(const PrefillParams &p, int s, int TM, int &base, int &count, int &parts,
+                                                 unsigned &bad) {
         const SeqRange r = seq_range<PAGED>(p, s, bad);
         count = (r.n + TM - 1) / TM;
-        base = max(r.keys - r.n, 0) / TM;
-    };
-    int base0 = 0, count0 = 0;
-    if (tid < B) level(tid, base0, count0);
-    int turn = 0;
-    auto above = [&](int d) {  // C(d)
-        int c = max(0, min(count0, base0 + count0 - d));
-        for (int s = tid + NT; s < B; s += NT) {
-            int b, n;
-            level(s, b, n);
-            c += max(0, min(n, b + n - d));
+        parts = PAGED ? parts_of(r.keys, p.split_tiles) : 1;
+        base = PAGED && p.split_tiles == 0 ? max(r.keys - r.n, 0) / TM : 0;
+    }
+
+    __device__ bool find(const PrefillParams &p, int k, int TM, Item &it, unsigned &bad) {
+        const int lane = threadIdx.x & 31, B = p.num_seqs, heads = p.num_kv_heads;
+        const bool split = PAGED && p.split_tiles > 0;
+        auto count_above = [&](int d, int *top) {  // C(d), and the highest level + 1
+            int c = 0, last = 0;
+            const int from = split ? 0 : start(d);
+            for (int s = lane; s < B; s += 32) {
+                int b, n, parts;
+                tiles(p, s, TM, b, n, parts, bad);
+                c += max(0, min(n, b + n - from)) * parts;
+                if (n > 0) last = max(last, split ? 1 : level_of(b + n - 1) + 1);
+            }
+            if (top) *top = __reduce_max_sync(FULL_MASK, last);
+            return (int)__reduce_add_sync(FULL_MASK, c);
+        };
+        int top;
+        if (k >= count_above(0, &top) * heads) return false;
+        if (level < 0) level = top;  // C = 0
+        int lo = 0, hi = level, before = above;  // C(lo) > k / heads >= C(hi) = before
+        for (int step = 1; hi - lo > 1;) {
+            const int mid = step < 4 ? max(hi - step, 1) : (lo + hi) >> 1;  // most often one of the next levels
+            step *= 2;
+            const int c = count_above(mid, nullptr);
+            if (c * heads > k) {
+                lo = mid;
+                step = 4;
+            } else {
+                hi = mid;
+                before = c;
+            }
         }
-        c = __reduce_add_sync(FULL_MASK, c);
-        int *w = scratch + (turn++ & 1) * 16;  // two buffers: one barrier a sum
-        if ((tid & 31) == 0) w[warp] = c;
-        __syncthreads();
-        int sum = 0;
+        level = hi;
+        above = before;
+        int rank = k - before * heads;  // within level lo
+        const int from = start(lo), to = start(lo + 1);
+        for (int s0 = 0; s0 < B; s0 += 32) {
+            const int s = s0 + lane;
+            int b = 0, n = 0, parts = 1, first = 0, last = 0;  // the sequence's tiles in this level
+            if (s < B) {
+                tiles(p, s, TM, b, n, parts, bad);
+                first = split ? 0 : max(from - b, 0);
+                last = split ? n : min(n, to - b);
+            }
+            const int mine = max(last - first, 0) * parts * heads;
+            int sum = mine;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) sum += w[i];
-        return sum;
-    };
-    if (k >= above(0)) return false;
-    int top = base0 + count0;
-    for (int s = tid + NT; s < B; s += NT) {
-        int b, n;
-        level(s, b, n);
-        top = max(top, b + n);
-    }
-    top = __reduce_max_sync(FULL_MASK, top);
-    {
-        int *w = scratch + (turn++ & 1) * 16;
-        if ((tid & 31) == 0) w[warp] = top;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NW; ++i) top = max(top, w[i]);
-    }
-    int lo = 0, hi = top, before = 0;  // C(lo) > k >= C(hi) = before
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        const int c = above(mid);
-        if (c > k) {
-            lo = mid;
-        } else {
-            hi = mid;
-            before = c;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(FULL_MASK, sum, o);
+                if (lane >= o) sum += up;
+            }
+            const unsigned m = __ballot_sync(FULL_MASK, sum > rank);
+            if (m) {
+                const int src = __ffs(m) - 1;
+                const int at = rank - __shfl_sync(FULL_MASK, sum - mine, src);
+                first = __shfl_sync(FULL_MASK, first, src);
+                last = __shfl_sync(FULL_MASK, last, src);
+                const int row = at / (last - first);  // part and head
+                it.s = s0 + src;
+                it.parts = __shfl_sync(FULL_MASK, parts, src);
+                it.kvh = row % heads;
+                it.part = row / heads;
+                it.tok0 = (last - 1 - at % (last - first)) * TM;
+                const SeqRange r = seq_range<PAGED>(p, it.s, bad);
+                it.row0 = r.row0;
+                it.n = r.n;
+                it.keys = r.keys;
+                return true;
+            }
+            rank -= __shfl_sync(FULL_MASK, sum, 31);
         }
+        return false;
     }
-    int rank = k - before;  // among the sequences with a tile at level lo, in order
-    for (int s0 = 0; s0 < B; s0 += NT) {
-        const int s = s0 + tid;
-        int b = base0, n = count0;
-        if (s0 && s < B) level(s, b, n);
-        const bool has = s < B && b <= lo && lo < b + n;
-        const unsigned m = __ballot_sync(FULL_MASK, has);
-        int *w = scratch + (turn++ & 1) * 16;
-        if ((tid & 31) == 0) w[warp] = __popc(m);
-        __syncthreads();
-        int prev = 0, all = 0;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            prev += i < warp ? w[i] : 0;
-            all += w[i];
-        }
-        if (has && prev + __popc(m & ((1u << (tid & 31)) - 1)) == rank) {
-            found[0] = s;
-            found[1] = (lo - b) * TM;
-        }
-        if (rank < all) break;
-        rank -= all;
-    }
-    __syncthreads();
-    tile.s = found[0];
-    tile.tok0 = found[1];
-    tile.r = seq_range<PAGED>(p, tile.s, bad);
-    return true;
-}
+};
 
 struct PrefillMaps {
     CUtensorMap q, k, v;
@@ -261,7 +396,7 @@ struct PrefillMaps {
 
 template <int D, typename T, bool PAGED, int NQ>
 __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
-    pa_prefill_mma_kernel(const PrefillParams p, const __grid_constant__ PrefillMaps maps, bool negate) {
+    pa_prefill_mma_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ PrefillMaps maps) {
     using SH = PrefillShape<D, NQ>;
     constexpr int HALVES = SH::HALVES, NS = SH::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -270,54 +405,44 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
     const uint32_t bars = base + SH::OFF_BAR;
     auto kv_full = [&](int i) { return bars + 8 * i; };
     auto kv_empty = [&](int i) { return bars + 8 * (NS + i); };
-    const uint32_t q_full = bars + 8 * (2 * NS);
-    auto s_full = [&](int t) { return bars + 8 * (2 * NS + 1 + t); };
-    auto p_full = [&](int t) { return bars + 8 * (2 * NS + 1 + NQ + t); };
-    auto o_full = [&](int t) { return bars + 8 * (2 * NS + 1 + 2 * NQ + t); };
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SH::OFF_MISC);
-    int *scratch = reinterpret_cast<int *>(smem + SH::OFF_MISC + 8);
-    int *found = scratch + 32;
+    const uint32_t item_full = bars + 8 * (2 * NS), item_empty = item_full + 8, next_full = item_full + 16;
+    auto stream_bar = [&](int k, int t) { return bars + 8 * (2 * NS + 3 + k * NQ + t); };
+    auto q_full = [&](int t) { return stream_bar(0, t); };
+    auto q_empty = [&](int t) { return stream_bar(1, t); };
+    auto s_full = [&](int t) { return stream_bar(2, t); };
+    auto p_most = [&](int t) { return stream_bar(3, t); };
+    auto p_full = [&](int t) { return stream_bar(4, t); };
+    auto o_full = [&](int t) { return stream_bar(5, t); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SH::OFF_TMEM);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(FULL_MASK, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int group = p.num_heads / p.num_kv_heads;
     const int tm = PF_BM / group;  // tokens of a tile of rows
-    const int kvh = blockIdx.x % p.num_kv_heads;
-    unsigned bad = 0;
-    TileAt tile;
-    const bool work =
-        locate_tile<PAGED, SH::THREADS>(p, blockIdx.x / p.num_kv_heads, NQ * tm, scratch, found, tile, bad);
-    if (bad) atomicOr(p.errors, bad);
-    bad = 0;
-    if (!work) return;
 
-    // Row i of the sequence's n sees the keys below first + i + 1.
-    const int first = tile.r.keys - tile.r.n;
-    int tiles[NQ], kv_end = 0, num_tiles = 0;
-#pragma unroll
-    for (int t = 0; t < NQ; ++t) {
-        const int a = tile.tok0 + t * tm, b = min(tile.r.n, a + tm);
-        const int end = a < b ? max(first + b, 0) : 0;
-        tiles[t] = (end + PF_BN - 1) / PF_BN;
-        kv_end = max(kv_end, end);
-        num_tiles = max(num_tiles, tiles[t]);
-    }
-
-    if (warp == NQ * 4) {
+    if (warp == SH::COPY_WARP) {
         if (lane == 0) {
             for (int i = 0; i < NS; ++i) {
                 mbar_init(kv_full(i), 1);
-                mbar_init(kv_empty(i), 1);
+                mbar_init(kv_empty(i), NQ);
             }
-            mbar_init(q_full, 1);
+            mbar_init(item_full, 1);
+            mbar_init(item_empty, SH::SOFTMAX_WARPS + 1 + NQ);
+            mbar_init(next_full, 1);
             for (int t = 0; t < NQ; ++t) {
+                mbar_init(q_full(t), 1);
+                mbar_init(q_empty(t), 1);
                 mbar_init(s_full(t), 1);
+                mbar_init(p_most(t), 4);
                 mbar_init(p_full(t), 4);
                 mbar_init(o_full(t), 1);
             }
             fence_barrier_init();
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
         }
         __syncwarp();
-    } else if (warp == NQ * 4 + 1) {
+    } else if (warp == SH::MMA_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "n"(SH::TMEM_COLS)
                      : "memory");
@@ -326,7 +451,7 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(FULL_MASK, *tmem_slot, 0);
 
     // A wait that runs out ends this warp's work: the error bit is set, later
     // waits and work are skipped, and the CTA still frees its TMEM.
@@ -338,249 +463,429 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
         }
         return alive;
     };
+    // The nth item, for every warp but the one that finds them.
+    auto next_item = [&](int nth, Item &it) {
+        if (!wait(item_full, nth & 1)) return false;
+        const int *at = reinterpret_cast<const int *>(smem + SH::OFF_ITEM);
+        it.s = __shfl_sync(FULL_MASK, at[0], 0);
+        it.tok0 = __shfl_sync(FULL_MASK, at[1], 0);
+        it.row0 = __shfl_sync(FULL_MASK, at[2], 0);
+        it.n = __shfl_sync(FULL_MASK, at[3], 0);
+        it.keys = __shfl_sync(FULL_MASK, at[4], 0);
+        it.part = __shfl_sync(FULL_MASK, at[5], 0);
+        it.parts = __shfl_sync(FULL_MASK, at[6], 0);
+        it.kvh = __shfl_sync(FULL_MASK, at[7], 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty);
+        return it.s >= 0;
+    };
 
-    if (warp == NQ * 4) {
-        // ---- copies ----
-        if (num_tiles > 0) {
-            if (lane == 0) {
-                uint32_t bytes = 0;
-                for (int t = 0; t < NQ; ++t) bytes += tiles[t] > 0 ? SH::TILE : 0;
-                mbar_arrive_expect_tx(q_full, bytes);
-                for (int t = 0; t < NQ; ++t)
-                    if (tiles[t] > 0)
-                        for (int h = 0; h < HALVES; ++h)
-                            tma_load_3d(base + t * SH::TILE + h * 16384, &maps.q, h * 64, kvh * group,
-                                        tile.r.row0 + tile.tok0 + t * tm, q_full);
-            }
-            __syncwarp();
-            int issued = 0;
-            const int per_tile = PAGED ? PF_BN / p.block_size : 0;
-            auto block_of = [&](int j) {  // this lane's block of key tile j
-                const int b = j * per_tile + lane;
-                int id = 0;
-                if (lane < per_tile && b * p.block_size < kv_end) {
-                    id = p.block_tables[(size_t)tile.s * p.max_blocks_per_seq + b];
-                    if ((unsigned)id >= (unsigned)p.num_blocks) {
-                        atomicOr(p.errors, PA_DEVERR_BLOCK_ID);
-                        id = 0;
-                    }
-                }
-                return id;
-            };
-            int id = 0, id_next = 0;
-            if constexpr (PAGED) id_next = block_of(0);
-            for (int c = 0; c < 2 * num_tiles; ++c) {
-                const int j = c >> 1, stage = c % NS;
-                if constexpr (PAGED) {
-                    if (!(c & 1)) {
-                        id = id_next;
-                        if (j + 1 < num_tiles) id_next = block_of(j + 1);
-                    }
-                }
-                if (c >= NS && !wait(kv_empty(stage), (c / NS - 1) & 1)) break;
-                const CUtensorMap *map = c & 1 ? &maps.v : &maps.k;
-                const uint32_t dst = base + SH::OFF_KV + stage * SH::TILE;
-                if constexpr (PAGED) {
-                    const int chunk = p.block_size * D * 2;
-                    const int blocks = min(per_tile, (kv_end - j * PF_BN + p.block_size - 1) / p.block_size);
-                    if (lane == 0) mbar_arrive_expect_tx(kv_full(stage), blocks * chunk);
-                    __syncwarp();
-                    if (lane < blocks)
-                        tma_load_chunk(dst + lane * chunk, map, id * p.num_kv_heads + kvh, kv_full(stage));
-                } else if (lane == 0) {
-                    mbar_arrive_expect_tx(kv_full(stage), SH::TILE);
-                    for (int h = 0; h < HALVES; ++h)
-                        tma_load_3d(dst + h * 16384, map, h * 64, kvh, tile.r.row0 + j * PF_BN, kv_full(stage));
+    if (warp >= SH::SOFTMAX_WARPS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SH::REGS_OTHER));
+        if (warp == SH::PLAN_WARP) {
+            // ---- finds the work items ----
+            Finder<PAGED> finder;
+            int index = blockIdx.x;
+            unsigned bad = 0;
+            for (int nth = 0;; ++nth) {
+                Item it;
+                bool work = index >= 0 && finder.find(p, index, NQ * tm, it, bad);
+                if (!work) it.s = -1;
+                if (nth == 0 && __any_sync(FULL_MASK, bad != 0) && bad) atomicOr(p.errors, bad);
+                if (lane == 0) {
+                    int *at = reinterpret_cast<int *>(smem + SH::OFF_ITEM);
+                    at[0] = it.s;
+                    at[1] = it.tok0;
+                    at[2] = it.row0;
+                    at[3] = it.n;
+                    at[4] = it.keys;
+                    at[5] = it.part;
+                    at[6] = it.parts;
+                    at[7] = it.kvh;
+                    mbar_arrive(item_full);
                 }
                 __syncwarp();
-                ++issued;
+                if (!work) break;
+                // When every warp has this item, the next launch is taken over.
+                if (!wait(item_empty, nth & 1)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(next_full, 16);
+                    asm volatile(
+                        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                        ::"r"(base + SH::OFF_NEXT), "r"(next_full)
+                        : "memory");
+                }
+                __syncwarp();
+                if (!wait(next_full, nth & 1)) break;
+                uint32_t taken, x;
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+                    "ld.shared.b128 r, [%2];\n\t"
+                    "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                    "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                    "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+                    : "=r"(taken), "=r"(x)
+                    : "r"(base + SH::OFF_NEXT)
+                    : "memory");
+                fence_proxy_async_smem();  // read before it is written again
+                index = __shfl_sync(FULL_MASK, taken ? (int)x : -1, 0);
             }
-            if (!alive)  // copies in flight land before the CTA leaves
-                for (int c = max(0, issued - NS); c < issued; ++c)
-                    mbar_wait_bounded(kv_full(c % NS), (c / NS) & 1, PF_WAIT_NS);
-        }
-    } else if (warp == NQ * 4 + 1) {
-        // ---- matrix instructions ----
-        // Instruction descriptor: 32-bit accumulator, both operands of the input
-        // type (0 fp16, 1 bf16), N / 8 at bit 17, M / 16 at bit 24; bit 13 negates
-        // A, bit 16 takes B with its columns contiguous.
-        constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-        constexpr uint32_t common = 1u << 4 | type << 7 | type << 10 | (uint32_t)(PF_BM >> 4) << 24;
-        const uint32_t idesc_qk = common | (uint32_t)(PF_BN >> 3) << 17 | (negate ? 1u << 13 : 0u);
-        constexpr uint32_t idesc_pv = common | (uint32_t)(D >> 3) << 17 | 1u << 16;
-        // Keys and values: rows of 128 bytes in groups of 8 (1024 bytes), for the
-        // packed form column after column, for the pools' chunks row group after row group.
-        constexpr uint32_t KV_GROUP = PAGED ? HALVES * 1024 : 1024, KV_HALF = PAGED ? 1024 : 16384;
-        auto qk = [&](int t, int stage) {
-            if (lane == 0) {
-                const uint32_t q = base + t * SH::TILE, k = base + SH::OFF_KV + stage * SH::TILE;
+        } else if (warp == SH::COPY_WARP) {
+            // ---- copies ----
+            Item it;
+            int c = 0, uses[NQ] = {};  // chunks (key or value tiles) issued; query tiles
+            for (int nth = 0; alive && next_item(nth, it); ++nth) {
+                const Walk<NQ> w = walk_of<NQ>(it, tm, p.split_tiles);
+#pragma unroll
+                for (int t = 0; t < NQ; ++t) {
+                    if (w.count[t] == 0) continue;
+                    if (uses[t] > 0 && !wait(q_empty(t), (uses[t] - 1) & 1)) break;
+                    ++uses[t];
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full(t), SH::TILE);
+                        for (int h = 0; h < HALVES; ++h)
+                            tma_load_3d(base + t * SH::TILE + h * 16384, &maps.q, h * 64, it.kvh * group,
+                                        it.row0 + it.tok0 + t * tm, q_full(t));
+                    }
+                    __syncwarp();
+                }
+                const int per_tile = PAGED ? PF_BN / p.block_size : 0;
+                auto block_of = [&](int j) {  // this lane's block of key tile j
+                    const int b = j * per_tile + lane;
+                    int id = 0;
+                    if (lane < per_tile && b * p.block_size < w.kv_end) {
+                        id = p.block_tables[(size_t)it.s * p.max_blocks_per_seq + b];
+                        if ((unsigned)id >= (unsigned)p.num_blocks) {
+                            atomicOr(p.errors, PA_DEVERR_BLOCK_ID);
+                            id = 0;
+                        }
+                    }
+                    return id;
+                };
+                int id_next = 0;
+                if constexpr (PAGED) id_next = block_of(w.j0);
+                for (int j = w.j0; j < w.j1 && alive; ++j) {
+                    const int id = id_next;
+                    if constexpr (PAGED) {
+                        if (j + 1 < w.j1) id_next = block_of(j + 1);
+                    }
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int stage = c % NS;
+                        if (c >= NS && !wait(kv_empty(stage), (c / NS - 1) & 1)) break;
+                        const CUtensorMap *map = kv ? &maps.v : &maps.k;
+                        const uint32_t dst = base + SH::OFF_KV + stage * SH::TILE;
+                        if constexpr (PAGED) {
+                            const int chunk = p.block_size * D * 2;
+                            const int blocks = min(per_tile, (w.kv_end - j * PF_BN + p.block_size - 1) / p.block_size);
+                            if (lane == 0) mbar_arrive_expect_tx(kv_full(stage), blocks * chunk);
+                            __syncwarp();
+                            if (lane < blocks)
+                                tma_load_chunk(dst + lane * chunk, map, id * p.num_kv_heads + it.kvh, kv_full(stage));
+                        } else if (lane == 0) {
+                            mbar_arrive_expect_tx(kv_full(stage), SH::TILE);
+                            for (int h = 0; h < HALVES; ++h)
+                                tma_load_3d(dst + h * 16384, map, h * 64, it.kvh, it.row0 + j * PF_BN, kv_full(stage));
+                        }
+                        __syncwarp();
+                        ++c;
+                    }
+                }
+            }
+            if (!alive) {  // copies in flight land before the CTA leaves
+                for (int i = max(0, c - NS); i < c; ++i) mbar_wait_bounded(kv_full(i % NS), (i / NS) & 1, PF_WAIT_NS);
+                for (int t = 0; t < NQ; ++t)
+                    if (uses[t] > 0) mbar_wait_bounded(q_full(t), (uses[t] - 1) & 1, PF_WAIT_NS);
+            }
+        } else if (warp < SH::MMA_WARP + NQ) {
+            // ---- matrix instructions: a warp for each tile of rows ----
+            // Instruction descriptor: 32-bit accumulator, both operands of the input
+            // type (0 fp16, 1 bf16), N / 8 at bit 17, M / 16 at bit 24; bit 13 negates
+            // A, bit 16 takes B with its columns contiguous.
+            constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+            constexpr uint32_t common = 1u << 4 | type << 7 | type << 10 | (uint32_t)(PF_BM >> 4) << 24;
+            const uint32_t idesc_qk = common | (uint32_t)(PF_BN >> 3) << 17 | (p.negate ? 1u << 13 : 0u);
+            constexpr uint32_t idesc_pv = common | (uint32_t)(D >> 3) << 17 | 1u << 16;
+            // Keys and values: rows of 128 bytes in groups of 8 (1024 bytes), for the
+            // packed form column after column, for the pools' chunks row group after row group.
+            constexpr uint32_t KV_GROUP = PAGED ? HALVES * 1024 : 1024, KV_HALF = PAGED ? 1024 : 16384;
+            const uint32_t one = elect_one();
+            const int t = warp - SH::MMA_WARP;
+            const uint32_t s_at = tmem + SH::S_COL + t * 128, o_at = tmem + SH::O_COL + t * D;
+            auto qk = [&](int stage) {
+                const uint32_t q = desc_lo(base + t * SH::TILE, 16), k = desc_lo(base + SH::OFF_KV + stage * SH::TILE, 16);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
-                    tc_mma(tmem + SH::S_COL + t * 128, smem_desc(q + (i >> 2) * 16384 + (i & 3) * 32, 16, 1024),
-                           smem_desc(k + (i >> 2) * KV_HALF + (i & 3) * 32, 16, KV_GROUP), idesc_qk, i > 0);
-                tc_commit(s_full(t));
-            }
-            __syncwarp();
-        };
-        if (num_tiles > 0 && wait(q_full, 0) && wait(kv_full(0), 0)) {
-            tc_fence_after();
-            for (int t = 0; t < NQ; ++t)
-                if (tiles[t] > 0) qk(t, 0);
-            if (lane == 0) tc_commit(kv_empty(0));
-            for (int j = 0; j < num_tiles && alive; ++j) {
-                const int cv = 2 * j + 1, sv = cv % NS, ck = cv + 1, sk = ck % NS;
-                if (!wait(kv_full(sv), (cv / NS) & 1)) break;
-                const uint32_t v = base + SH::OFF_KV + sv * SH::TILE;
-                if (PAGED && kv_end < (j + 1) * PF_BN) {
-                    // Slots behind the context hold anything: their weights are 0, their values made 0.
-                    for (int i = (kv_end - j * PF_BN) * HALVES * 8 + lane; i < PF_BN * HALVES * 8; i += 32) {
-                        const int row = i / (HALVES * 8), c = i % (HALVES * 8);
-                        const uint32_t at = v + (row >> 3) * KV_GROUP + (c >> 3) * KV_HALF + (row & 7) * 128 + (c & 7) * 16;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                    tc_mma(s_at, q + ((i >> 2) * 16384 + (i & 3) * 32) / 16, desc_hi(1024),
+                           k + ((i >> 2) * KV_HALF + (i & 3) * 32) / 16, desc_hi(KV_GROUP), idesc_qk, i > 0, one);
+                tc_commit(s_full(t), one);
+            };
+            Item it;
+            int c = 0, uses = 0, weights = 0;  // chunks taken, query tiles, tiles of weights
+            for (int nth = 0; alive && next_item(nth, it); ++nth) {
+                const Walk<NQ> w = walk_of<NQ>(it, tm, p.split_tiles);
+                const int mine = t == 0 ? w.count[0] : w.count[NQ - 1], tiles = w.j1 - w.j0;
+                if (tiles == 0) continue;
+                if (mine > 0 && !wait(q_full(t), uses & 1)) break;
+                if (!wait(kv_full(c % NS), (c / NS) & 1)) break;
+                if (mine > 0) {
+                    ++uses;
+                    qk(c % NS);
+                    if (mine == 1) tc_commit(q_empty(t), one);
                 }
-                const bool more = j + 1 < num_tiles;
-                if (more && !wait(kv_full(sk), (ck / NS) & 1)) break;
-                for (int t = 0; t < NQ; ++t) {
-                    if (j >= tiles[t]) continue;
-                    if (!wait(p_full(t), j & 1)) break;
-                    tc_fence_after();
-                    if (lane == 0) {
+                tc_commit(kv_empty(c % NS), one);
+                ++c;
+                for (int j = 0; j < tiles; ++j) {
+                    const int sv = c % NS, sk = (c + 1) % NS;
+                    if (!wait(kv_full(sv), (c / NS) & 1)) break;
+                    const uint32_t v = base + SH::OFF_KV + sv * SH::TILE;
+                    const int left = w.kv_end - (w.j0 + j) * PF_BN;
+                    if (PAGED && left < PF_BN) {
+                        // Slots behind the context hold anything: their weights are 0, their values made 0.
+                        for (int i = left * HALVES * 8 + lane; i < PF_BN * HALVES * 8; i += 32) {
+                            const int row = i / (HALVES * 8), col = i % (HALVES * 8);
+                            const uint32_t at =
+                                v + (row >> 3) * KV_GROUP + (col >> 3) * KV_HALF + (row & 7) * 128 + (col & 7) * 16;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    const bool more = j + 1 < tiles;
+                    if (more && !wait(kv_full(sk), ((c + 1) / NS) & 1)) break;
+                    if (j < mine) {
+                        const uint32_t vd = desc_lo(v, KV_HALF);
+                        auto pv = [&](int i) {  // keys 16 i to 16 i + 15
+                            tc_mma_ta(o_at, s_at + i * 8, vd + i * 2 * KV_GROUP / 16, desc_hi(KV_GROUP), idesc_pv,
+                                      j > 0 || i > 0, one);
+                        };
+                        // The product starts on the first three quarters of the weights.
+                        if (!wait(p_most(t), weights & 1)) break;
+                        tc_fence_after();
 #pragma unroll
-                        for (int i = 0; i < PF_BN / 16; ++i)
-                            tc_mma_ta(tmem + SH::O_COL + t * D, tmem + SH::S_COL + t * 128 + i * 8,
-                                      smem_desc(v + i * 2 * KV_GROUP, KV_HALF, KV_GROUP), idesc_pv, j > 0 || i > 0);
-                        if (j + 1 == tiles[t]) tc_commit(o_full(t));
+                        for (int i = 0; i < 6; ++i) pv(i);
+                        if (!wait(p_full(t), weights & 1)) break;
+                        tc_fence_after();
+                        pv(6);
+                        pv(7);
+                        ++weights;
+                        if (j + 1 < mine) {
+                            qk(sk);
+                            if (j + 2 == mine) tc_commit(q_empty(t), one);
+                        } else {
+                            tc_commit(o_full(t), one);
+                        }
                     }
-                    __syncwarp();
-                    if (j + 1 < tiles[t]) qk(t, sk);
+                    tc_commit(kv_empty(sv), one);
+                    ++c;
+                    if (more) {
+                        tc_commit(kv_empty(sk), one);
+                        ++c;
+                    }
                 }
-                if (lane == 0 && alive) {
-                    tc_commit(kv_empty(sv));
-                    if (more) tc_commit(kv_empty(sk));
-                }
-                __syncwarp();
             }
         }
-    } else if (warp < NQ * 4) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SH::REGS_SOFTMAX));
         // ---- softmax: a thread for each row ----
         const int t = warp >> 2, quarter = warp & 3;
-        const int r = t * PF_BM + quarter * 32 + lane;  // row of the CTA
-        const int tok = tile.tok0 + r / group, head = kvh * group + r % group;
-        const bool valid = tok < tile.r.n;
-        const int visible = valid ? max(first + tok + 1, 0) : 0;
-        const int clear = max(first + tile.tok0 + (t * PF_BM + quarter * 32) / group + 1, 0);  // seen by all the warp's rows
+        const int r = t * PF_BM + quarter * 32 + lane;  // row of the item
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_addr = lanes + SH::S_COL + t * 128, o_addr = lanes + SH::O_COL + t * D;
-        const int n_tiles = t == 0 ? tiles[0] : tiles[NQ - 1];
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-        float m = -INFINITY, l = 0.f;  // m: what the weights are relative to, unscaled
-        for (int j = 0; j < n_tiles; ++j) {
-            if (!wait(s_full(t), j & 1)) break;
-            tc_fence_after();
-            float x[PF_BN];
+        Item it;
+        int scores = 0, results = 0;  // tiles of scores taken, accumulators read
+        for (int nth = 0; alive && next_item(nth, it); ++nth) {
+            const Walk<NQ> w = walk_of<NQ>(it, tm, p.split_tiles);
+            const int mine = t == 0 ? w.count[0] : w.count[NQ - 1];
+            const int tok = it.tok0 + r / group, head = it.kvh * group + r % group;
+            const bool valid = tok < it.n;
+            const int visible = valid ? max(w.first + tok + 1, 0) : 0;
+            const int clear = max(w.first + it.tok0 + (r - lane) / group + 1, 0);  // seen by all the warp's rows
+            float m = -INFINITY, l = 0.f;  // m: what the weights are relative to, unscaled
+            for (int j = 0; j < mine; ++j) {
+                if (!wait(s_full(t), scores & 1)) break;
+                ++scores;
+                tc_fence_after();
+                float x[4][32];
 #pragma unroll
-            for (int c = 0; c < PF_BN; c += 32) tc_ld32(s_addr + c, x + c);
-            tc_landed(x);
-            if ((j + 1) * PF_BN > clear) {
-                const int left = visible - j * PF_BN;
+                for (int c = 0; c < 4; ++c) tc_ld32(s_addr + c * 32, x[c]);
+                tc_landed(x[0]);
 #pragma unroll
-                for (int c = 0; c < PF_BN; ++c) x[c] = c < left ? x[c] : -INFINITY;
-            }
-            float mx[4] = {x[0], x[1], x[2], x[3]};
+                for (int c = 1; c < 4; ++c) tc_pin(x[c]);
+                const int key0 = (w.j0 + j) * PF_BN;
+                if (key0 + PF_BN > clear) {
+                    const int left = visible - key0;
 #pragma unroll
-            for (int c = 4; c < PF_BN; c += 4)
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], x[c + i]);
-            const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-            const bool grow = (top - m) * p.scale_log2 > 8.f;
-            if (__any_sync(FULL_MASK, grow)) {
-                const float f = grow ? ex2((m - top) * p.scale_log2) : 1.f;
-                m = grow ? top : m;
-                l *= f;
-                if (j > 0) {
+                        for (int i = 0; i < 32; ++i) x[c][i] = c * 32 + i < left ? x[c][i] : -INFINITY;
+                }
+                float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[c][i], x[c][i + 1]);
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                const bool grow = (top - m) * p.scale_log2 > 8.f;
+                if (__any_sync(FULL_MASK, grow)) {
+                    const float f = grow ? ex2((m - top) * p.scale_log2) : 1.f;
+                    m = grow ? top : m;
+                    l *= f;
+                    if (j > 0) {
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        tc_ld32(o_addr + c, o);
-                        tc_landed(o);
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tc_ld32(o_addr + c, o);
+                            tc_landed(o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= f;
-                        tc_st32(o_addr + c, reinterpret_cast<uint32_t *>(o));
+                            for (int i = 0; i < 32; ++i) o[i] *= f;
+                            tc_st32(o_addr + c, reinterpret_cast<uint32_t *>(o));
+                        }
                     }
                 }
-            }
-            const float ref = m == -INFINITY ? 0.f : -m * p.scale_log2;  // nothing above -inf yet: weights 0
-            const float2 ref2 = make_float2(ref, ref);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float ref = m == -INFINITY ? 0.f : -m * p.scale_log2;  // nothing above -inf yet: weights 0
+                const float2 ref2 = make_float2(ref, ref);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < PF_BN; c += 64) {
-                uint32_t w[32];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t y16[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float2 y = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), scale2, ref2);
-                    y.x = ex2(y.x);
-                    y.y = ex2(y.y);
-                    sum[i & 1] = add2(sum[i & 1], y);
-                    w[i] = Elem<T>::pack(y.x, y.y);
+                    for (int i = 0; i < 16; ++i) {
+                        float2 y = fma2(make_float2(x[c][2 * i], x[c][2 * i + 1]), scale2, ref2);
+                        if (i * PF_POLY % 16 < PF_POLY)
+                            y = ex2_fma<T>(y);
+                        else
+                            y = make_float2(ex2(y.x), ex2(y.y));
+                        sum[i & 1] = add2(sum[i & 1], y);
+                        y16[i] = Elem<T>::pack(y.x, y.y);
+                    }
+                    tc_st16(s_addr + c * 16, y16);
+                    if (c >= 2) {
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(c == 2 ? p_most(t) : p_full(t));
+                    }
                 }
-                tc_st32(s_addr + c / 2, w);
+                const float2 both = add2(sum[0], sum[1]);
+                l += both.x + both.y;
             }
-            const float2 both = add2(sum[0], sum[1]);
-            l += both.x + both.y;
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full(t));
-        }
-        // ---- epilogue ----
-        const float inv = 1.f / l;
-        bool again = visible > 0 && !(l > 0.f && l < INFINITY);
-        if (n_tiles > 0) wait(o_full(t), 0);
-        tc_fence_after();
-        T *out = static_cast<T *>(p.out) + ((size_t)(tile.r.row0 + tok) * p.num_heads + head) * D;
-        if (alive) {
+            // ---- the item's rows ----
+            const int lo = w.j0 * PF_BN, hi = min(visible, w.j1 * PF_BN);  // keys the row has seen here
+            const bool some = hi > lo;
+            const float inv = some ? (it.parts > 1 ? 1.f : 1.f / l) : 0.f;
+            bool again = some && !(l > 0.f && l < INFINITY);
+            if (mine > 0) {
+                if (!wait(o_full(t), results & 1)) break;
+                ++results;
+                tc_fence_after();
+            }
+            const size_t at = (size_t)(it.row0 + tok) * p.num_heads + head;
+            const size_t part_at = (size_t)it.part * p.num_tokens * p.num_heads + at;
             float nan = 0.f;
-            uint32_t w[D / 2];
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
-                if (n_tiles > 0) {
+                if (mine > 0) {
                     tc_ld32(o_addr + c, o);
                     tc_landed(o);
                 }
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float a = visible > 0 ? o[i] * inv : 0.f, b = visible > 0 ? o[i + 1] * inv : 0.f;
-                    nan = fmaf(a, 0.f, fmaf(b, 0.f, nan));
-                    w[(c + i) / 2] = Elem<T>::pack(a, b);
+                for (int i = 0; i < 32; ++i) {
+                    o[i] = some ? o[i] * inv : 0.f;
+                    nan = fmaf(o[i], 0.f, nan);
                 }
-            }
-            again = again || (visible > 0 && !(nan == 0.f));
-            if (valid && !again) {
+                __syncwarp();
+                if (!valid) {
+                    // rows of no token: nothing to store
+                } else if (PAGED && it.parts > 1) {
+                    float4 *out = reinterpret_cast<float4 *>(p.part_acc + part_at * D + c);
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    reinterpret_cast<uint4 *>(out)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    for (int i = 0; i < 8; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                } else {
+                    using E = Elem<T>;
+                    uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + at * D + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        out[i] = make_uint4(E::pack(o[8 * i], o[8 * i + 1]), E::pack(o[8 * i + 2], o[8 * i + 3]),
+                                            E::pack(o[8 * i + 4], o[8 * i + 5]), E::pack(o[8 * i + 6], o[8 * i + 7]));
+                }
+                __syncwarp();
             }
-            // A row of floats for each warp, in the tile of queries: its products are done.
-            float *q_row = reinterpret_cast<float *>(smem + t * SH::TILE) + quarter * D;
-            for (unsigned m_again = __ballot_sync(FULL_MASK, again); m_again; m_again &= m_again - 1) {
-                const int from = __ffs(m_again) - 1;
-                attend_row<D, T, PAGED>(p, tile.s, tile.r.row0 + __shfl_sync(FULL_MASK, tok, from),
-                                        __shfl_sync(FULL_MASK, head, from), __shfl_sync(FULL_MASK, visible, from), q_row,
-                                        negate, bad);
+            if (PAGED && it.parts > 1 && valid)
+                p.part_ml[part_at] = make_float2(some ? m * p.scale_log2 : -INFINITY, some ? l : 0.f);
+            again = again || !(nan == 0.f);
+            tc_fence_before();
+            __syncwarp();
+            for (unsigned rows = __ballot_sync(FULL_MASK, again); rows; rows &= rows - 1) {
+                const int src = __ffs(rows) - 1;
+                const int row = it.row0 + __shfl_sync(FULL_MASK, tok, src), h = __shfl_sync(FULL_MASK, head, src);
+                const RowPart<D> part =
+                    attend_row<D, T, PAGED>(p, it.s, it.row0, row, h, lo, __shfl_sync(FULL_MASK, hi, src));
+                store_row<D, T>(p, row, h, it.part, it.parts, part);
             }
-            if (bad) atomicOr(p.errors, bad);
         }
-        tc_fence_before();
     }
     __syncthreads();
-    if (warp == NQ * 4 + 1) {
+    if (warp == SH::MMA_WARP) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(SH::TMEM_COLS));
     }
+}
+
+// Joins the parts of split contexts: a warp for each (token, head) row.
+//   out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i
+template <int D, typename T>
+__global__ void __launch_bounds__(256) pa_prefill_join_kernel(const __grid_constant__ PrefillParams p) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (item >= (long long)p.num_tokens * p.num_heads) return;
+    const int row = (int)(item / p.num_heads);
+    int lo = 0, hi = p.num_seqs;  // the last sequence that starts at or before the row
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu_seqlens[mid] <= row)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    unsigned bad = 0;
+    const SeqRange r = seq_range<true>(p, lo, bad);
+    if (row < r.row0 || row >= r.row0 + r.n) return;
+    const int parts = parts_of(r.keys, p.split_tiles);
+    if (parts == 1) return;
+    const size_t stride = (size_t)p.num_tokens * p.num_heads;
+    float m = -INFINITY, l = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[i * stride + item].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float2 ml = p.part_ml[i * stride + item];
+        const float *a = p.part_acc + (i * stride + item) * D + lane * E;
+        float x[E];
+        if constexpr (E == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(a);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(a);
+            x[0] = v.x, x[1] = v.y;
+        }
+        const float f = exp2f(ml.x - ref);
+        l = fmaf(ml.y, f, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], f, acc[e]);
+    }
+    const bool some = r.keys - r.n + (row - r.row0) + 1 > 0;
+    const float inv = some ? 1.f / l : 0.f;
+    uint32_t *op = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + (size_t)item * D) + lane * (E / 2);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) op[e] = Elem<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
 }
 
 }  // namespace pa
