@@ -572,34 +572,66 @@ def pa_decode_noalloc(out, q, k_pool, v_pool, block_tables, context_lens, scale,
     return out
 
 
-def _tensors(*named, device=None) -> torch.device:
-    """Checks (tensor, name, shape or None, dtype) tuples: CUDA, contiguous, one device. Returns that device."""
-    for t, name, shape, dtype in named:
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name} must be a CUDA tensor")
-        _cuda(t, name, dtype)
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if device is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {device}")
-        device = t.device
-    return device
+
+# ---- the prompt path ----------------------------------------------------------------------------------
+# A step makes several of these calls, each of a few microseconds on the device, so their checks are
+# kept to what one attribute look-up each can see.
+
+def _complain(t, name, shape, dtype, dev) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _stream_of(device, stream) -> int:
-    """The given stream, or the current stream of the tensors' device."""
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+def _full(t, name, shape, dtype, dev) -> int:
+    """Data pointer of a contiguous CUDA tensor of this shape, type and device."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _complain(t, name, shape, dtype, dev)
 
 
-def _rows(t, name, heads, head_dim, dtype, device) -> int:
+def _rows(t, name, shape, dtype, dev) -> int:
     """Token stride of [T][heads][D] rows whose heads and elements are contiguous (tokens may be further apart)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
-        raise ValueError(f"{name} must be a CUDA tensor [T][{heads}][{head_dim}]")
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} on {device}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        raise ValueError(f"{name} must be a CUDA tensor of shape {tuple(shape)}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} on cuda:{dev}")
+    T, h, D = shape
+    st, sh, se = t.stride()
+    if se != 1 or (h > 1 and sh != D):
         raise ValueError(f"{name}: a token's heads and elements must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+    return st if T > 1 else h * D
+
+
+def _heads(q, name="q"):
+    """Shape, type code and device of [T][H][D] query rows."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [T][H][D]")
+    code = _DTYPES.get(q.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be fp16 or bf16")
+    return q.shape, code, q.get_device()
+
+
+def _call(fn, dev, stream, *args) -> None:
+    """fn(*args, stream) with the tensors' device current, on the given stream or that device's current one."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != PA_OK:
+        _check(status)
 
 
 def pa_assign_slots(block_tables, free_blocks, context_lens, num_free, new_lens, block_size, slot_mapping, positions,
@@ -611,24 +643,23 @@ def pa_assign_slots(block_tables, free_blocks, context_lens, num_free, new_lens,
     (-1 behind the last token), cu_seqlens int32 [B + 1], and the new lengths and free count, in place unless
     context_lens_out / num_free_out are given.
     """
-    context_lens_out = context_lens if context_lens_out is None else context_lens_out
-    num_free_out = num_free if num_free_out is None else num_free_out
-    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2 or free_blocks.dim() != 1:
-        raise ValueError("block_tables must be [B][W] and free_blocks [NB]")
-    B, W = block_tables.shape
-    T = slot_mapping.numel()
-    i32 = torch.int32
-    dev = _tensors((block_tables, "block_tables", None, i32), (free_blocks, "free_blocks", None, i32),
-                   (context_lens, "context_lens", (B,), i32), (num_free, "num_free", (1,), i32),
-                   (new_lens, "new_lens", (B,), i32), (slot_mapping, "slot_mapping", (T,), torch.int64),
-                   (positions, "positions", (T,), i32), (cu_seqlens, "cu_seqlens", (B + 1,), i32),
-                   (context_lens_out, "context_lens_out", (B,), i32), (num_free_out, "num_free_out", (1,), i32))
-    with torch.cuda.device(dev):
-        _check(lib().pa_assign_slots(
-            block_tables.data_ptr(), free_blocks.data_ptr(), context_lens_out.data_ptr(), num_free_out.data_ptr(),
-            slot_mapping.data_ptr(), positions.data_ptr(), cu_seqlens.data_ptr(), context_lens.data_ptr(),
-            num_free.data_ptr(), new_lens.data_ptr(), B, W, int(block_size), free_blocks.numel(), T,
-            _stream_of(dev, stream)))
+    if not isinstance(block_tables, torch.Tensor) or not block_tables.is_cuda or block_tables.dim() != 2:
+        raise ValueError("block_tables must be a CUDA tensor [B][W]")
+    if not isinstance(free_blocks, torch.Tensor) or free_blocks.dim() != 1:
+        raise ValueError("free_blocks must be [NB]")
+    if not isinstance(slot_mapping, torch.Tensor) or slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [T]")
+    dev, i32 = block_tables.get_device(), torch.int32
+    B, W = shape = block_tables.shape
+    NB, T = free_blocks.shape[0], slot_mapping.shape[0]
+    tables = _full(block_tables, "block_tables", shape, i32, dev)
+    ctx, nf = _full(context_lens, "context_lens", (B,), i32, dev), _full(num_free, "num_free", (1,), i32, dev)
+    ctx_out = ctx if context_lens_out is None else _full(context_lens_out, "context_lens_out", (B,), i32, dev)
+    nf_out = nf if num_free_out is None else _full(num_free_out, "num_free_out", (1,), i32, dev)
+    _call(lib().pa_assign_slots, dev, stream, tables, _full(free_blocks, "free_blocks", (NB,), i32, dev), ctx_out, nf_out,
+          _full(slot_mapping, "slot_mapping", (T,), torch.int64, dev), _full(positions, "positions", (T,), i32, dev),
+          _full(cu_seqlens, "cu_seqlens", (B + 1,), i32, dev), ctx, nf, _full(new_lens, "new_lens", (B,), i32, dev),
+          B, W, block_size, NB, T)
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, inv_freq, mscale=1.0,
@@ -640,41 +671,33 @@ def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, i
     the token is skipped), slot_mapping int64 [T] (negative: no cache write). Without a cache v, k_pool, v_pool and
     slot_mapping are None and k_out is needed.
     """
-    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q must be [T][H][D] and k [T][Hkv][D]")
-    T, H, D = q.shape
-    Hkv = k.shape[1]
-    if q.dtype not in _DTYPES:
-        raise ValueError("q must be fp16 or bf16")
-    dt, dev = q.dtype, q.device
-    cache = [v, k_pool, v_pool, slot_mapping]
-    if any(x is None for x in cache) and not all(x is None for x in cache):
-        raise ValueError("v, k_pool, v_pool and slot_mapping go together")
-    qs, ks = _rows(q, "q", H, D, dt, dev), _rows(k, "k", Hkv, D, dt, dev)
-    if k.shape[0] != T:
-        raise ValueError("q and k differ in tokens")
-    need = [(q_out, "q_out", (T, H, D), dt), (positions, "positions", (T,), torch.int32),
-            (inv_freq, "inv_freq", None, torch.float64)]
-    if k_out is not None:
-        need.append((k_out, "k_out", (T, Hkv, D), dt))
-    vs, NB, bs = 0, 0, 16
-    if v is not None:
-        vs = _rows(v, "v", Hkv, D, dt, dev)
-        if v.shape[0] != T or k_pool.dim() != 4:
-            raise ValueError("v must be [T][Hkv][D] and the pools [NB][Hkv][bs][D]")
+    q_shape, code, dev = _heads(q)
+    T, H, D = q_shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [T][Hkv][D]")
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot_dim / 2]")
+    dt, Hkv = q.dtype, k.shape[1]
+    kv_shape = (T, Hkv, D)
+    qs, ks, vs, NB, bs = _rows(q, "q", q_shape, dt, dev), _rows(k, "k", kv_shape, dt, dev), 0, 0, 16
+    vp = kp = vpool = slots = None
+    if v is not None and k_pool is not None and v_pool is not None and slot_mapping is not None:
+        vs = _rows(v, "v", kv_shape, dt, dev)
+        if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+            raise ValueError("the pools must be [NB][Hkv][bs][D]")
         NB, _, bs, _ = k_pool.shape
-        need += [(k_pool, "k_pool", (NB, Hkv, bs, D), dt), (v_pool, "v_pool", (NB, Hkv, bs, D), dt),
-                 (slot_mapping, "slot_mapping", (T,), torch.int64)]
-    _tensors(*need, device=dev)
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
-
-    with torch.cuda.device(dev):
-        _check(lib().pa_rope_and_cache(
-            ptr(q_out), ptr(k_out), ptr(q), ptr(k), ptr(v), ptr(k_pool), ptr(v_pool), ptr(positions),
-            ptr(slot_mapping), ptr(inv_freq), T, H, Hkv, D, 2 * inv_freq.numel(), int(bool(interleaved)), bs, NB, qs, ks,
-            vs, float(mscale), _DTYPES[dt], _stream_of(dev, stream)))
+        pool = (NB, Hkv, bs, D)
+        vp, kp = v.data_ptr(), _full(k_pool, "k_pool", pool, dt, dev)
+        vpool = _full(v_pool, "v_pool", pool, dt, dev)
+        slots = _full(slot_mapping, "slot_mapping", (T,), torch.int64, dev)
+    elif not (v is None and k_pool is None and v_pool is None and slot_mapping is None):
+        raise ValueError("v, k_pool, v_pool and slot_mapping go together")
+    half = inv_freq.shape[0]
+    _call(lib().pa_rope_and_cache, dev, stream, _full(q_out, "q_out", q_shape, dt, dev),
+          None if k_out is None else _full(k_out, "k_out", kv_shape, dt, dev), q.data_ptr(), k.data_ptr(), vp, kp, vpool,
+          _full(positions, "positions", (T,), torch.int32, dev), slots,
+          _full(inv_freq, "inv_freq", (half,), torch.float64, dev), T, H, Hkv, D, 2 * half, 1 if interleaved else 0, bs,
+          NB, qs, ks, vs, mscale, code)
     return q_out
 
 
@@ -683,28 +706,23 @@ def pa_prefill(out, q, k, v, cu_seqlens, scale, stream=None) -> torch.Tensor:
     cu_seqlens[s + 1] (int32 [B + 1]) of q [T][H][D] and k, v [T][Hkv][D] (fp16 or bf16, tokens any stride apart).
     Writes those rows of out [T][H][D]; other rows stay as they were.
     """
-    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q must be [T][H][D] and k [T][Hkv][D]")
-    T, H, D = q.shape
-    Hkv = k.shape[1]
-    if q.dtype not in _DTYPES:
-        raise ValueError("q must be fp16 or bf16")
-    qs = _rows(q, "q", H, D, q.dtype, q.device)
-    ks, vs = _rows(k, "k", Hkv, D, q.dtype, q.device), _rows(v, "v", Hkv, D, q.dtype, q.device)
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError("q, k and v differ in tokens")
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    shape, code, dev = _heads(q)
+    T, H, D = shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [T][Hkv][D]")
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [B + 1]")
-    _tensors((out, "out", (T, H, D), q.dtype), (cu_seqlens, "cu_seqlens", None, torch.int32), device=q.device)
-    with torch.cuda.device(q.device):
-        _check(lib().pa_prefill(
-            out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T,
-            H, Hkv, D, qs, ks, vs, float(scale), _DTYPES[q.dtype], _stream_of(q.device, stream)))
+    dt, Hkv, n = q.dtype, k.shape[1], cu_seqlens.shape[0]
+    kv_shape = (T, Hkv, D)
+    qs, ks, vs = _rows(q, "q", shape, dt, dev), _rows(k, "k", kv_shape, dt, dev), _rows(v, "v", kv_shape, dt, dev)
+    _call(lib().pa_prefill, dev, stream, _full(out, "out", shape, dt, dev), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          _full(cu_seqlens, "cu_seqlens", (n,), torch.int32, dev), n - 1, T, H, Hkv, D, qs, ks, vs, scale, code)
     return out
 
 
 def pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
                                     max_context_len) -> int:
+    """Workspace bytes of pa_prefill_paged on the current device."""
     n = int(lib().pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
                                                   max_context_len))
     if n == 0:
@@ -715,9 +733,10 @@ def pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_head
 def alloc_prefill_workspace(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
                             device=None) -> torch.Tensor:
     """Workspace for pa_prefill_paged."""
-    n = pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
-                                        max_context_len)
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    with torch.cuda.device(device):
+        n = pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
+                                            max_context_len)
+        return torch.empty(n, dtype=torch.uint8, device="cuda")
 
 
 def pa_prefill_paged(out, q, k_pool, v_pool, block_tables, context_lens, cu_seqlens, scale, max_context_len,
@@ -726,31 +745,26 @@ def pa_prefill_paged(out, q, k_pool, v_pool, block_tables, context_lens, cu_seql
     of q [T][H][D] are the last ones of its context_lens[s] cached tokens. Pools, tables and lengths as pa_decode
     (16-bit cache); writes those rows of out [T][H][D], other rows stay as they were.
     """
-    if not isinstance(q, torch.Tensor) or not isinstance(k_pool, torch.Tensor) or q.dim() != 3 or k_pool.dim() != 4:
-        raise ValueError("q must be [T][H][D] and the pools [NB][Hkv][bs][D]")
-    T, H, D = q.shape
-    NB, Hkv, bs, _ = k_pool.shape
-    if q.dtype not in _DTYPES:
-        raise ValueError("q must be fp16 or bf16")
-    qs = _rows(q, "q", H, D, q.dtype, q.device)
+    shape, code, dev = _heads(q)
+    T, H, D = shape
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+        raise ValueError("the pools must be [NB][Hkv][bs][D]")
     if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
         raise ValueError("block_tables must be [B][W]")
-    B, W = block_tables.shape
-    _tensors((out, "out", (T, H, D), q.dtype), (k_pool, "k_pool", (NB, Hkv, bs, D), q.dtype),
-             (v_pool, "v_pool", (NB, Hkv, bs, D), q.dtype), (block_tables, "block_tables", None, torch.int32),
-             (context_lens, "context_lens", (B,), torch.int32), (cu_seqlens, "cu_seqlens", (B + 1,), torch.int32),
-             device=q.device)
-    with torch.cuda.device(q.device):
-        st = _stream_of(q.device, stream)
-        if workspace is None:
-            workspace = alloc_prefill_workspace(B, T, H, Hkv, D, bs, max_context_len, q.device)
-            if st != torch.cuda.current_stream(q.device).cuda_stream:
-                # Allocated on the current stream, used on another: kept until that one has passed.
-                workspace.record_stream(torch.cuda.ExternalStream(st, device=q.device))
-        else:
-            _tensors((workspace, "workspace", None, None), device=q.device)
-        _check(lib().pa_prefill_paged(
-            out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
-            context_lens.data_ptr(), cu_seqlens.data_ptr(), B, T, H, Hkv, D, bs, W, NB, int(max_context_len), qs,
-            float(scale), _DTYPES[q.dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size(), st))
+    dt, i32 = q.dtype, torch.int32
+    NB, Hkv, bs, _ = k_pool.shape
+    pool = (NB, Hkv, bs, D)
+    B, W = tables = block_tables.shape
+    if workspace is None:
+        workspace = alloc_prefill_workspace(B, T, H, Hkv, D, bs, max_context_len, dev)
+        if stream is not None:
+            # Allocated on the current stream, used on another: kept until that one has passed.
+            workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), device=dev))
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    _call(lib().pa_prefill_paged, dev, stream, _full(out, "out", shape, dt, dev), q.data_ptr(),
+          _full(k_pool, "k_pool", pool, dt, dev), _full(v_pool, "v_pool", pool, dt, dev),
+          _full(block_tables, "block_tables", tables, i32, dev), _full(context_lens, "context_lens", (B,), i32, dev),
+          _full(cu_seqlens, "cu_seqlens", (B + 1,), i32, dev), B, T, H, Hkv, D, bs, W, NB, max_context_len,
+          _rows(q, "q", shape, dt, dev), scale, code, workspace.data_ptr(), workspace.nbytes)
     return out

@@ -241,8 +241,10 @@ pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const v
         return fail(PA_ERR_INVALID, "misaligned pointer (16 B tensors, 4 B int arrays, 256 B workspace)");
     if (q_stride % 8 || q_stride < (long long)num_heads * head_dim)
         return fail(PA_ERR_INVALID, "the token stride must be a multiple of 8 and hold a token's heads");
+    if (workspace_bytes < 256) return fail(PA_ERR_INVALID, "workspace %zu bytes < 256", workspace_bytes);
     const size_t need = pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
                                                         block_size, max_context_len);
+    if (need == 0) return PA_ERR_CUDA;  // no device; pa_last_error() has the reason
     if (workspace_bytes < need)
         return fail(PA_ERR_INVALID, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     pa::PrefillParams p{};

@@ -186,6 +186,13 @@ __device__ __forceinline__ void tma_load_chunk(uint32_t dst, const CUtensorMap *
         : "memory");
 }
 
+// 32 bytes at once: a whole sector of a row, where each lane has a row.
+__device__ __forceinline__ void store_32b(void *at, const uint32_t *x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -263,7 +270,7 @@ template <int NQ>
 struct Walk {
     int first;            // row i of the sequence sees the keys below first + i + 1
     int j0, j1, kv_end;   // kv_end: the keys that any of the rows sees
-    int count[NQ];
+    int count[NQ], end[NQ];  // end: the keys that any row of the tile sees
 };
 
 template <int NQ>
@@ -277,6 +284,7 @@ __device__ __forceinline__ Walk<NQ> walk_of(const Item &it, int tm, int split_ti
         const int a = it.tok0 + t * tm, b = min(it.n, a + tm);
         const int end = a < b ? max(w.first + b, 0) : 0;
         tiles[t] = (end + PF_BN - 1) / PF_BN;
+        w.end[t] = end;
         w.kv_end = max(w.kv_end, end);
     }
     const int all = (w.kv_end + PF_BN - 1) / PF_BN;
@@ -303,7 +311,8 @@ __device__ __forceinline__ int parts_of(int keys, int split_tiles) {
 // C(d + 1) <= k / heads < C(d). One warp; its calls come with growing k.
 template <bool PAGED>
 struct Finder {
-    int level = -1, above = 0;  // C(level) = above <= the last k / heads
+    int level = -1, above = 0, all = 0;  // C(level) = above <= the last k / heads; C(0) = all
+    int4 mine;                  // this lane's sequence among the first 32: base, count, parts
 
     __device__ __forceinline__ static int start(int d) { return d < 8 ? d : 8 * (d - 7); }
     __device__ __forceinline__ static int level_of(int position) { return position < 8 ? position : 7 + position / 8; }
@@ -323,17 +332,20 @@ struct Finder {
             int c = 0, last = 0;
             const int from = split ? 0 : start(d);
             for (int s = lane; s < B; s += 32) {
-                int b, n, parts;
-                tiles(p, s, TM, b, n, parts, bad);
+                int b = mine.x, n = mine.y, parts = mine.z;
+                if (s >= 32) tiles(p, s, TM, b, n, parts, bad);
                 c += max(0, min(n, b + n - from)) * parts;
                 if (n > 0) last = max(last, split ? 1 : level_of(b + n - 1) + 1);
             }
             if (top) *top = __reduce_max_sync(FULL_MASK, last);
             return (int)__reduce_add_sync(FULL_MASK, c);
         };
-        int top;
-        if (k >= count_above(0, &top) * heads) return false;
-        if (level < 0) level = top;  // C = 0
+        if (level < 0) {
+            mine = make_int4(0, 0, 1, 0);
+            if (lane < B) tiles(p, lane, TM, mine.x, mine.y, mine.z, bad);
+            all = count_above(0, &level);  // C(level) = 0
+        }
+        if (k >= all * heads) return false;
         int lo = 0, hi = level, before = above;  // C(lo) > k / heads >= C(hi) = before
         for (int step = 1; hi - lo > 1;) {
             const int mid = step < 4 ? max(hi - step, 1) : (lo + hi) >> 1;  // most often one of the next levels
@@ -355,7 +367,8 @@ struct Finder {
             const int s = s0 + lane;
             int b = 0, n = 0, parts = 1, first = 0, last = 0;  // the sequence's tiles in this level
             if (s < B) {
-                tiles(p, s, TM, b, n, parts, bad);
+                b = mine.x, n = mine.y, parts = mine.z;
+                if (s >= 32) tiles(p, s, TM, b, n, parts, bad);
                 first = split ? 0 : max(from - b, 0);
                 last = split ? n : min(n, to - b);
             }
@@ -536,10 +549,8 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
             int c = 0, uses[NQ] = {};  // chunks (key or value tiles) issued; query tiles
             for (int nth = 0; alive && next_item(nth, it); ++nth) {
                 const Walk<NQ> w = walk_of<NQ>(it, tm, p.split_tiles);
-#pragma unroll
-                for (int t = 0; t < NQ; ++t) {
-                    if (w.count[t] == 0) continue;
-                    if (uses[t] > 0 && !wait(q_empty(t), (uses[t] - 1) & 1)) break;
+                auto queries = [&](int t) {
+                    if (w.count[t] == 0 || (uses[t] > 0 && !wait(q_empty(t), (uses[t] - 1) & 1))) return;
                     ++uses[t];
                     if (lane == 0) {
                         mbar_arrive_expect_tx(q_full(t), SH::TILE);
@@ -548,7 +559,8 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                                         it.row0 + it.tok0 + t * tm, q_full(t));
                     }
                     __syncwarp();
-                }
+                };
+                queries(0);
                 const int per_tile = PAGED ? PF_BN / p.block_size : 0;
                 auto block_of = [&](int j) {  // this lane's block of key tile j
                     const int b = j * per_tile + lane;
@@ -589,6 +601,9 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                         }
                         __syncwarp();
                         ++c;
+                        // The second tile of rows still multiplies the last item's keys: its
+                        // queries come behind the first keys.
+                        if (NQ == 2 && kv == 0 && j == w.j0) queries(NQ - 1);
                     }
                 }
             }
@@ -604,7 +619,7 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
             // A, bit 16 takes B with its columns contiguous.
             constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
             constexpr uint32_t common = 1u << 4 | type << 7 | type << 10 | (uint32_t)(PF_BM >> 4) << 24;
-            const uint32_t idesc_qk = common | (uint32_t)(PF_BN >> 3) << 17 | (p.negate ? 1u << 13 : 0u);
+            const uint32_t idesc_qk = common | (p.negate ? 1u << 13 : 0u);  // and N
             constexpr uint32_t idesc_pv = common | (uint32_t)(D >> 3) << 17 | 1u << 16;
             // Keys and values: rows of 128 bytes in groups of 8 (1024 bytes), for the
             // packed form column after column, for the pools' chunks row group after row group.
@@ -612,12 +627,13 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
             const uint32_t one = elect_one();
             const int t = warp - SH::MMA_WARP;
             const uint32_t s_at = tmem + SH::S_COL + t * 128, o_at = tmem + SH::O_COL + t * D;
-            auto qk = [&](int stage) {
+            auto qk = [&](int stage, int cols) {  // cols: keys, a multiple of 16
+                const uint32_t idesc = idesc_qk | (uint32_t)(cols >> 3) << 17;
                 const uint32_t q = desc_lo(base + t * SH::TILE, 16), k = desc_lo(base + SH::OFF_KV + stage * SH::TILE, 16);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
                     tc_mma(s_at, q + ((i >> 2) * 16384 + (i & 3) * 32) / 16, desc_hi(1024),
-                           k + ((i >> 2) * KV_HALF + (i & 3) * 32) / 16, desc_hi(KV_GROUP), idesc_qk, i > 0, one);
+                           k + ((i >> 2) * KV_HALF + (i & 3) * 32) / 16, desc_hi(KV_GROUP), idesc, i > 0, one);
                 tc_commit(s_full(t), one);
             };
             Item it;
@@ -626,11 +642,14 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                 const Walk<NQ> w = walk_of<NQ>(it, tm, p.split_tiles);
                 const int mine = t == 0 ? w.count[0] : w.count[NQ - 1], tiles = w.j1 - w.j0;
                 if (tiles == 0) continue;
+                // Keys of tile j that any row of this one sees, in the steps of 16 of the products.
+                const int end = t == 0 ? w.end[0] : w.end[NQ - 1];
+                auto cols = [&](int j) { return min((end - (w.j0 + j) * PF_BN + 15) & ~15, PF_BN); };
                 if (mine > 0 && !wait(q_full(t), uses & 1)) break;
                 if (!wait(kv_full(c % NS), (c / NS) & 1)) break;
                 if (mine > 0) {
                     ++uses;
-                    qk(c % NS);
+                    qk(c % NS, cols(0));
                     if (mine == 1) tc_commit(q_empty(t), one);
                 }
                 tc_commit(kv_empty(c % NS), one);
@@ -659,18 +678,20 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                             tc_mma_ta(o_at, s_at + i * 8, vd + i * 2 * KV_GROUP / 16, desc_hi(KV_GROUP), idesc_pv,
                                       j > 0 || i > 0, one);
                         };
+                        const int steps = cols(j) / 16;
                         // The product starts on the first three quarters of the weights.
                         if (!wait(p_most(t), weights & 1)) break;
                         tc_fence_after();
 #pragma unroll
-                        for (int i = 0; i < 6; ++i) pv(i);
+                        for (int i = 0; i < 6; ++i)
+                            if (i < steps) pv(i);
                         if (!wait(p_full(t), weights & 1)) break;
                         tc_fence_after();
-                        pv(6);
-                        pv(7);
+                        if (steps > 6) pv(6);
+                        if (steps > 7) pv(7);
                         ++weights;
                         if (j + 1 < mine) {
-                            qk(sk);
+                            qk(sk, cols(j + 1));
                             if (j + 2 == mine) tc_commit(q_empty(t), one);
                         } else {
                             tc_commit(o_full(t), one);
@@ -693,6 +714,7 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_addr = lanes + SH::S_COL + t * 128, o_addr = lanes + SH::O_COL + t * D;
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+        const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
         Item it;
         int scores = 0, results = 0;  // tiles of scores taken, accumulators read
         for (int nth = 0; alive && next_item(nth, it); ++nth) {
@@ -701,7 +723,9 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
             const int tok = it.tok0 + r / group, head = it.kvh * group + r % group;
             const bool valid = tok < it.n;
             const int visible = valid ? max(w.first + tok + 1, 0) : 0;
-            const int clear = max(w.first + it.tok0 + (r - lane) / group + 1, 0);  // seen by all the warp's rows
+            // Keys that all of the warp's rows see, and that any does.
+            const int clear = max(w.first + it.tok0 + (r - lane) / group + 1, 0);
+            const int seen = max(w.first + min(it.tok0 + (r - lane + 31) / group, it.n - 1) + 1, 0);
             float m = -INFINITY, l = 0.f;  // m: what the weights are relative to, unscaled
             for (int j = 0; j < mine; ++j) {
                 if (!wait(s_full(t), scores & 1)) break;
@@ -714,7 +738,8 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
 #pragma unroll
                 for (int c = 1; c < 4; ++c) tc_pin(x[c]);
                 const int key0 = (w.j0 + j) * PF_BN;
-                if (key0 + PF_BN > clear) {
+                const bool masked = key0 + PF_BN > clear;
+                if (masked) {
                     const int left = visible - key0;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -747,8 +772,7 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                 const float ref = m == -INFINITY ? 0.f : -m * p.scale_log2;  // nothing above -inf yet: weights 0
                 const float2 ref2 = make_float2(ref, ref);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                auto weigh = [&](int c) {
                     uint32_t y16[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -761,12 +785,37 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                         y16[i] = Elem<T>::pack(y.x, y.y);
                     }
                     tc_st16(s_addr + c * 16, y16);
-                    if (c >= 2) {
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(c == 2 ? p_most(t) : p_full(t));
-                    }
+                };
+                auto ready = [&](uint32_t bar) {
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                };
+                if (!masked) {
+                    weigh(0);
+                    weigh(1);
+                    weigh(2);
+                    ready(p_most(t));
+                    weigh(3);
+                    ready(p_full(t));
+                } else {
+                    // Keys that none of the warp's rows sees weigh 0.
+                    const int some = seen - key0;
+                    auto weigh_some = [&](int c) {
+                        if (c * 32 < some) {
+                            weigh(c);
+                        } else {
+                            const uint32_t zero[16] = {};
+                            tc_st16(s_addr + c * 16, zero);
+                        }
+                    };
+                    weigh_some(0);
+                    weigh_some(1);
+                    weigh_some(2);
+                    ready(p_most(t));
+                    weigh_some(3);
+                    ready(p_full(t));
                 }
                 const float2 both = add2(sum[0], sum[1]);
                 l += both.x + both.y;
@@ -800,16 +849,23 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                 if (!valid) {
                     // rows of no token: nothing to store
                 } else if (PAGED && it.parts > 1) {
-                    float4 *out = reinterpret_cast<float4 *>(p.part_acc + part_at * D + c);
+                    uint32_t *out = reinterpret_cast<uint32_t *>(p.part_acc + part_at * D + c);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int i = 0; i < 32; i += 8) store_32b(out + i, reinterpret_cast<uint32_t *>(o) + i);
                 } else {
-                    using E = Elem<T>;
-                    uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + at * D + c);
+                    uint32_t y[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        out[i] = make_uint4(E::pack(o[8 * i], o[8 * i + 1]), E::pack(o[8 * i + 2], o[8 * i + 3]),
-                                            E::pack(o[8 * i + 4], o[8 * i + 5]), E::pack(o[8 * i + 6], o[8 * i + 7]));
+                    for (int i = 0; i < 16; ++i) y[i] = Elem<T>::pack(o[2 * i], o[2 * i + 1]);
+                    T *out = static_cast<T *>(p.out) + at * D + c;
+                    if (wide) {
+                        store_32b(out, y);
+                        store_32b(out + 16, y + 8);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            reinterpret_cast<uint4 *>(out)[i] =
+                                make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    }
                 }
                 __syncwarp();
             }
