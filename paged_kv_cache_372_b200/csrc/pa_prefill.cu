@@ -43,9 +43,15 @@ pa_status encode_pool(PFN_cuTensorMapEncodeTiled enc, CUtensorMap *map, CUtensor
 
 constexpr int kMaxDevices = 64;
 
+// Contexts are split where there are fewer items than kSplitItems an SM (a paged
+// call of few rows), into parts of kSplitTiles key tiles at least; a part costs
+// about kPartTiles key tiles beside its own (its start and end, its partial result).
+constexpr long long kSplitItems = 6;
+constexpr int kSplitTiles = 4, kPartTiles = 4;
+
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-template <int D, typename T, bool PAGED, int NQ>
+template <int D, typename T, bool PAGED>
 pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
     int dev, sms;
     pa_status st = pa_internal_device(&dev, &sms);
@@ -71,8 +77,8 @@ pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
             PA_OK)
             return st;
     }
-    using SH = pa::PrefillShape<D, NQ>;
-    auto kernel = pa::pa_prefill_mma_kernel<D, T, PAGED, NQ>;
+    using SH = pa::PrefillShape<D>;
+    auto kernel = pa::pa_prefill_mma_kernel<D, T, PAGED>;
     static std::atomic<bool> done[kMaxDevices];
     if (!done[dev].load(std::memory_order_acquire)) {
         cudaFuncAttributes attr;
@@ -86,7 +92,7 @@ pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
         done[dev].store(true, std::memory_order_release);
     }
     // Every sequence has at most one tile that is not full.
-    const int tokens = NQ * pa::PF_BM / group;
+    const int tokens = pa::PF_NQ * pa::PF_BM / group;
     const long long grid =
         (p.num_tokens / tokens + (long long)std::min(p.num_seqs, p.num_tokens)) * p.num_kv_heads * max_parts;
     if (grid >= (1ll << 31)) return fail(PA_ERR_UNSUPPORTED, "too many tiles");
@@ -104,37 +110,41 @@ pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
     return PA_OK;
 }
 
-template <bool PAGED, int NQ>
+template <bool PAGED>
 pa_status dispatch(pa::PrefillParams &p, int head_dim, int dtype, int max_parts, cudaStream_t s) {
     if (head_dim == 128)
-        return dtype == PA_F16 ? launch<128, __half, PAGED, NQ>(p, max_parts, s)
-                               : launch<128, __nv_bfloat16, PAGED, NQ>(p, max_parts, s);
-    return dtype == PA_F16 ? launch<64, __half, PAGED, NQ>(p, max_parts, s)
-                           : launch<64, __nv_bfloat16, PAGED, NQ>(p, max_parts, s);
+        return dtype == PA_F16 ? launch<128, __half, PAGED>(p, max_parts, s)
+                               : launch<128, __nv_bfloat16, PAGED>(p, max_parts, s);
+    return dtype == PA_F16 ? launch<64, __half, PAGED>(p, max_parts, s)
+                           : launch<64, __nv_bfloat16, PAGED>(p, max_parts, s);
 }
 
-// How a call is cut up: tiles of rows of an item, key tiles of a part (0: contexts
-// are not split) and the parts the longest context gives.
+// How contexts are split: key tiles of a part (0: they are not) and the parts
+// the longest one gives.
 struct Cut {
-    int nq, split_tiles, max_parts;
+    int split_tiles, max_parts;
 };
 
-Cut cut_of(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int max_keys, bool paged, int sms) {
-    Cut c{2, 0, 1};
+Cut cut_of(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int max_keys, int sms) {
     const long long rows = (long long)num_tokens * (num_heads / num_kv_heads);
-    if (rows <= (long long)num_seqs * pa::PF_BM) c.nq = 1;
-    if (!paged) return c;
-    const long long slots = (long long)sms * (c.nq == 1 ? 2 : 1);
     const long long items =
-        std::max<long long>(std::min(num_seqs, num_tokens), ceil_div(rows, c.nq * pa::PF_BM)) * num_kv_heads;
+        std::max<long long>(std::min(num_seqs, num_tokens), ceil_div(rows, pa::PF_NQ * pa::PF_BM)) * num_kv_heads;
     const int tiles = (int)ceil_div(max_keys, pa::PF_BN);
-    if (items < 4 * slots && tiles > 8) {
-        const long long parts = std::min<long long>(ceil_div(4 * slots, items), tiles / 8);
-        c.split_tiles = (int)ceil_div(tiles, parts);
-        c.max_parts = (int)ceil_div(tiles, c.split_tiles);
-        if (c.max_parts == 1) c.split_tiles = 0;
+    if (items >= kSplitItems * sms || tiles < 2 * kSplitTiles) return Cut{0, 1};
+    // Rounds of the SMs times the key tiles of a part, with what a part costs beside them.
+    const long long least = ceil_div(kSplitItems * sms, items);
+    long long best = 0, split = tiles;
+    for (long long parts = least; parts <= 4 * least && parts * kSplitTiles <= tiles; ++parts) {
+        const long long part = ceil_div(tiles, parts);
+        const long long cost = ceil_div(items * parts, sms) * (part + kPartTiles);
+        if (best == 0 || cost < best) {
+            best = cost;
+            split = part;
+        }
     }
-    return c;
+    if (best == 0) split = kSplitTiles;  // too short for that: the shortest parts
+    const int max_parts = (int)ceil_div(tiles, split);
+    return max_parts > 1 ? Cut{(int)split, max_parts} : Cut{0, 1};
 }
 
 template <bool PAGED>
@@ -146,8 +156,7 @@ pa_status run(pa::PrefillParams &p, const Cut &cut, int head_dim, float scale, i
     p.scale_log2 = a < FLT_MIN ? FLT_MIN : a;
     p.negate = scale < 0.f;
     p.split_tiles = cut.split_tiles;
-    return cut.nq == 1 ? dispatch<PAGED, 1>(p, head_dim, dtype, cut.max_parts, s)
-                       : dispatch<PAGED, 2>(p, head_dim, dtype, cut.max_parts, s);
+    return dispatch<PAGED>(p, head_dim, dtype, cut.max_parts, s);
 }
 
 bool heads_supported(int num_heads, int num_kv_heads) {
@@ -203,8 +212,7 @@ pa_status pa_prefill(void *out, const void *q, const void *k, const void *v, con
     p.k_stride = k_stride;
     p.v_stride = v_stride;
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
-    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, num_tokens, false, 0);
-    return run<false>(p, cut, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
+    return run<false>(p, Cut{0, 1}, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
 }
 
 size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
@@ -216,7 +224,7 @@ size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_hea
     if (num_seqs == 0 || num_tokens == 0) return 256;
     int dev, sms;
     if (pa_internal_device(&dev, &sms) != PA_OK) return 0;
-    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, true, sms);
+    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, sms);
     if (cut.max_parts == 1) return 256;
     const size_t rows = (size_t)num_tokens * num_heads * cut.max_parts;
     return align256(rows * sizeof(float2)) + rows * head_dim * sizeof(float);
@@ -268,7 +276,7 @@ pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const v
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
     int dev, sms;
     if ((st = pa_internal_device(&dev, &sms)) != PA_OK) return st;
-    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, true, sms);
+    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, sms);
     const size_t rows = (size_t)num_tokens * num_heads * cut.max_parts;
     p.part_ml = static_cast<float2 *>(workspace);
     p.part_acc = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align256(rows * sizeof(float2)));

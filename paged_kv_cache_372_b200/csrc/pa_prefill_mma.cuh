@@ -1,6 +1,6 @@
 // Tensor-core kernel of pa_prefill and pa_prefill_paged (include/pa.h).
 //
-// A work item is NQ tiles of 128 query rows of one (sequence, KV head), walked
+// A work item is two tiles of 128 query rows of one (sequence, KV head), walked
 // over the keys they see in tiles of 128. The rows are (token, query head) pairs
 // of the group, head fastest: all query heads of a KV head share its key and value
 // tiles, and a tile spans few tokens, so little of it is masked. For each tile
@@ -38,35 +38,34 @@
 
 namespace pa {
 
+constexpr int PF_NQ = 2;    // tiles of rows of an item
 constexpr int PF_BM = 128;  // rows of a tile
 constexpr int PF_BN = 128;  // keys of a tile
 constexpr int PF_POLY = 4;  // of 16 pairs of exponentials, those on the FMA units
 constexpr uint64_t PF_WAIT_NS = 4000000000ull;
 
-template <int D, int NQ>
+template <int D>
 struct PrefillShape {
     static constexpr int HALVES = D / 64;     // 128-byte columns of a row
     static constexpr int TILE = 128 * D * 2;  // bytes of a tile of rows (queries, keys or values)
-    static constexpr int SOFTMAX_WARPS = NQ * 4;
+    static constexpr int SOFTMAX_WARPS = PF_NQ * 4;
     static constexpr int COPY_WARP = SOFTMAX_WARPS, MMA_WARP = COPY_WARP + 1, PLAN_WARP = COPY_WARP + 3;
     static constexpr int THREADS = SOFTMAX_WARPS * 32 + 128;
-    // NQ = 2: one CTA an SM; NQ = 1: two.
-    static constexpr int STAGES = NQ == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 5);
-    // Registers move from the other warps to the softmax warps:
-    // 384 threads x 168 = 256 x 216 + 128 x 72, 256 threads x 128 = 128 x 200 + 128 x 56.
-    static constexpr int REGS_LAUNCH = NQ == 2 ? 168 : 128;
-    static constexpr int REGS_SOFTMAX = NQ == 2 ? 216 : 200, REGS_OTHER = NQ == 2 ? 72 : 56;
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    // Registers move from the other warps to the softmax warps: 384 threads x 168 = 256 x 216 + 128 x 72.
+    static constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 216, REGS_OTHER = 72;
     static_assert(SOFTMAX_WARPS * 32 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * REGS_LAUNCH,
                   "more registers than launched");
-    static constexpr int TMEM_COLS = NQ == 2 ? 512 : 256;
-    static constexpr int S_COL = 0, O_COL = NQ * 128;
-    static constexpr int OFF_KV = NQ * TILE;
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int S_COL = 0, O_COL = PF_NQ * 128;
+    static constexpr int OFF_KV = PF_NQ * TILE;
     static constexpr int OFF_NEXT = OFF_KV + STAGES * TILE;  // 16 bytes: the launch taken over
     static constexpr int OFF_ITEM = OFF_NEXT + 16;           // the work item, 8 integers
     static constexpr int OFF_TMEM = OFF_ITEM + 32;           // TMEM address
     static constexpr int OFF_BAR = OFF_TMEM + 16;
-    static constexpr int NUM_BARS = 2 * STAGES + 3 + 6 * NQ;
-    static constexpr int BYTES = OFF_BAR + NUM_BARS * 8 + 1024;  // and slack for the alignment to 1024
+    static constexpr int NUM_BARS = 2 * STAGES + 5 + 6 * PF_NQ;
+    static constexpr int OFF_SWAP = OFF_BAR + (NUM_BARS + 1) / 2 * 16;  // the second tile's maxima and sums
+    static constexpr int BYTES = OFF_SWAP + PF_BM * 8 + 1024;           // and slack for the alignment to 1024
 };
 
 // ---- tcgen05 ------------------------------------------------------------------------------------------
@@ -78,6 +77,9 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
 // `one` is set; the whole warp runs the code around them, so that descriptors
 // and addresses stay in uniform registers. (Issued under a branch of one lane,
 // 8 instructions took 650 to 970 clocks to issue, more than they run.)
+// A value that all lanes have, as a uniform register (a warp reduction leaves it in one).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(FULL_MASK, x); }
+
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t one;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
@@ -265,33 +267,42 @@ struct Item {
     int part, parts, kvh;   // part of the context and their number, KV head
 };
 
-// Key tiles an item walks, [j0, j1), and those of its tiles of rows among them.
-template <int NQ>
+// Key tiles an item walks, [j0, j1), and how its two tiles of rows share them:
+// each walks all that its rows see. Where the second has no rows (the last rows of
+// a prompt, few rows over a long context) both take the first one's rows, one the
+// even and one the odd key tiles, and their results are joined at the end: one
+// tile of rows alone would wait for its softmax half of the time.
 struct Walk {
-    int first;            // row i of the sequence sees the keys below first + i + 1
-    int j0, j1, kv_end;   // kv_end: the keys that any of the rows sees
-    int count[NQ], end[NQ];  // end: the keys that any row of the tile sees
+    int first;           // row i of the sequence sees the keys below first + i + 1
+    int j0, j1, kv_end;  // kv_end: the keys that any of the rows sees
+    bool halves;
+    int count[PF_NQ], end[PF_NQ];  // key tiles of a tile of rows, the keys that any of its rows sees
 };
 
-template <int NQ>
-__device__ __forceinline__ Walk<NQ> walk_of(const Item &it, int tm, int split_tiles) {
-    Walk<NQ> w;
+// halves: whether items may be walked in halves (few rows over a paged context).
+__device__ __forceinline__ Walk walk_of(const Item &it, int tm, int split_tiles, bool halves) {
+    Walk w;
     w.first = it.keys - it.n;
     w.kv_end = 0;
-    int tiles[NQ];
+    int tiles[PF_NQ];
 #pragma unroll
-    for (int t = 0; t < NQ; ++t) {
+    for (int t = 0; t < PF_NQ; ++t) {
         const int a = it.tok0 + t * tm, b = min(it.n, a + tm);
-        const int end = a < b ? max(w.first + b, 0) : 0;
-        tiles[t] = (end + PF_BN - 1) / PF_BN;
-        w.end[t] = end;
-        w.kv_end = max(w.kv_end, end);
+        w.end[t] = a < b ? max(w.first + b, 0) : 0;
+        tiles[t] = (w.end[t] + PF_BN - 1) / PF_BN;
+        w.kv_end = max(w.kv_end, w.end[t]);
     }
     const int all = (w.kv_end + PF_BN - 1) / PF_BN;
     w.j0 = it.parts > 1 ? min(it.part * split_tiles, all) : 0;
     w.j1 = it.parts > 1 ? min(w.j0 + split_tiles, all) : all;
 #pragma unroll
-    for (int t = 0; t < NQ; ++t) w.count[t] = max(min(tiles[t], w.j1) - w.j0, 0);
+    for (int t = 0; t < PF_NQ; ++t) w.count[t] = max(min(tiles[t], w.j1) - w.j0, 0);
+    w.halves = halves && it.tok0 + tm >= it.n && w.count[0] > 1;
+    if (w.halves) {
+        w.count[1] = w.count[0] / 2;
+        w.count[0] -= w.count[1];
+        w.end[1] = w.end[0];
+    }
     return w;
 }
 
@@ -407,19 +418,20 @@ struct PrefillMaps {
     CUtensorMap q, k, v;
 };
 
-template <int D, typename T, bool PAGED, int NQ>
-__global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
+template <int D, typename T, bool PAGED>
+__global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
     pa_prefill_mma_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ PrefillMaps maps) {
-    using SH = PrefillShape<D, NQ>;
-    constexpr int HALVES = SH::HALVES, NS = SH::STAGES;
+    using SH = PrefillShape<D>;
+    constexpr int HALVES = SH::HALVES, NS = SH::STAGES, NQ = PF_NQ;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     const uint32_t base = smem_u32(smem);
     const uint32_t bars = base + SH::OFF_BAR;
     auto kv_full = [&](int i) { return bars + 8 * i; };
     auto kv_empty = [&](int i) { return bars + 8 * (NS + i); };
-    const uint32_t item_full = bars + 8 * (2 * NS), item_empty = item_full + 8, next_full = item_full + 16;
-    auto stream_bar = [&](int k, int t) { return bars + 8 * (2 * NS + 3 + k * NQ + t); };
+    const uint32_t item_full = bars + 8 * (2 * NS), item_empty = item_full + 8, next_full = item_full + 16,
+                   pair_full = item_full + 24, pair_empty = item_full + 32;
+    auto stream_bar = [&](int k, int t) { return bars + 8 * (2 * NS + 5 + k * NQ + t); };
     auto q_full = [&](int t) { return stream_bar(0, t); };
     auto q_empty = [&](int t) { return stream_bar(1, t); };
     auto s_full = [&](int t) { return stream_bar(2, t); };
@@ -441,6 +453,8 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
             mbar_init(item_full, 1);
             mbar_init(item_empty, SH::SOFTMAX_WARPS + 1 + NQ);
             mbar_init(next_full, 1);
+            mbar_init(pair_full, 4);
+            mbar_init(pair_empty, 4);
             for (int t = 0; t < NQ; ++t) {
                 mbar_init(q_full(t), 1);
                 mbar_init(q_empty(t), 1);
@@ -548,7 +562,7 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
             Item it;
             int c = 0, uses[NQ] = {};  // chunks (key or value tiles) issued; query tiles
             for (int nth = 0; alive && next_item(nth, it); ++nth) {
-                const Walk<NQ> w = walk_of<NQ>(it, tm, p.split_tiles);
+                const Walk w = walk_of(it, tm, p.split_tiles, PAGED);
                 auto queries = [&](int t) {
                     if (w.count[t] == 0 || (uses[t] > 0 && !wait(q_empty(t), (uses[t] - 1) & 1))) return;
                     ++uses[t];
@@ -556,7 +570,7 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                         mbar_arrive_expect_tx(q_full(t), SH::TILE);
                         for (int h = 0; h < HALVES; ++h)
                             tma_load_3d(base + t * SH::TILE + h * 16384, &maps.q, h * 64, it.kvh * group,
-                                        it.row0 + it.tok0 + t * tm, q_full(t));
+                                        it.row0 + it.tok0 + (w.halves ? 0 : t * tm), q_full(t));
                     }
                     __syncwarp();
                 };
@@ -603,7 +617,7 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                         ++c;
                         // The second tile of rows still multiplies the last item's keys: its
                         // queries come behind the first keys.
-                        if (NQ == 2 && kv == 0 && j == w.j0) queries(NQ - 1);
+                        if (kv == 0 && j == w.j0) queries(1);
                     }
                 }
             }
@@ -626,7 +640,7 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
             constexpr uint32_t KV_GROUP = PAGED ? HALVES * 1024 : 1024, KV_HALF = PAGED ? 1024 : 16384;
             const uint32_t one = elect_one();
             const int t = warp - SH::MMA_WARP;
-            const uint32_t s_at = tmem + SH::S_COL + t * 128, o_at = tmem + SH::O_COL + t * D;
+            const uint32_t s_at = uniform(tmem + SH::S_COL + t * 128), o_at = uniform(tmem + SH::O_COL + t * D);
             auto qk = [&](int stage, int cols) {  // cols: keys, a multiple of 16
                 const uint32_t idesc = idesc_qk | (uint32_t)(cols >> 3) << 17;
                 const uint32_t q = desc_lo(base + t * SH::TILE, 16), k = desc_lo(base + SH::OFF_KV + stage * SH::TILE, 16);
@@ -636,19 +650,74 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                            k + ((i >> 2) * KV_HALF + (i & 3) * 32) / 16, desc_hi(KV_GROUP), idesc, i > 0, one);
                 tc_commit(s_full(t), one);
             };
+            int weights = 0;  // tiles of weights taken
+            // The product with the values in a stage; there: keys of the tile below kv_end.
+            auto pv = [&](int stage, int there, int cols, bool add) {
+                const uint32_t v = base + SH::OFF_KV + stage * SH::TILE, vd = desc_lo(v, KV_HALF);
+                if (PAGED && there < PF_BN) {
+                    // Slots behind the context hold anything: their weights are 0, their values made 0.
+                    for (int i = there * HALVES * 8 + lane; i < PF_BN * HALVES * 8; i += 32) {
+                        const int row = i / (HALVES * 8), col = i % (HALVES * 8);
+                        const uint32_t at = v + (row >> 3) * KV_GROUP + (col >> 3) * KV_HALF + (row & 7) * 128 + (col & 7) * 16;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                auto step = [&](int i) {  // keys 16 i to 16 i + 15
+                    tc_mma_ta(o_at, s_at + i * 8, vd + i * 2 * KV_GROUP / 16, desc_hi(KV_GROUP), idesc_pv, add || i > 0,
+                              one);
+                };
+                const int steps = cols / 16;
+                // The product starts on the first three quarters of the weights.
+                if (!wait(p_most(t), weights & 1)) return;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < 6; ++i)
+                    if (i < steps) step(i);
+                if (!wait(p_full(t), weights & 1)) return;
+                tc_fence_after();
+                if (steps > 6) step(6);
+                if (steps > 7) step(7);
+                ++weights;
+            };
             Item it;
-            int c = 0, uses = 0, weights = 0;  // chunks taken, query tiles, tiles of weights
+            int c = 0, uses = 0;  // chunks taken, query tiles
             for (int nth = 0; alive && next_item(nth, it); ++nth) {
-                const Walk<NQ> w = walk_of<NQ>(it, tm, p.split_tiles);
-                const int mine = t == 0 ? w.count[0] : w.count[NQ - 1], tiles = w.j1 - w.j0;
+                const Walk w = walk_of(it, tm, p.split_tiles, PAGED);
+                const int tiles = w.j1 - w.j0, mine = t == 0 ? w.count[0] : w.count[1];
                 if (tiles == 0) continue;
                 // Keys of tile j that any row of this one sees, in the steps of 16 of the products.
-                const int end = t == 0 ? w.end[0] : w.end[NQ - 1];
+                const int end = t == 0 ? w.end[0] : w.end[1];
                 auto cols = [&](int j) { return min((end - (w.j0 + j) * PF_BN + 15) & ~15, PF_BN); };
-                if (mine > 0 && !wait(q_full(t), uses & 1)) break;
+                auto there = [&](int j) { return w.kv_end - (w.j0 + j) * PF_BN; };
+                if (mine > 0) {
+                    if (!wait(q_full(t), uses & 1)) break;
+                    ++uses;
+                }
+                if (PAGED && w.halves) {
+                    // Every other key tile, chunks in their order.
+                    for (int j = 0; j < tiles; ++j, c += 2) {
+                        const bool own = (j & 1) == t;
+                        const int sk = c % NS, sv = (c + 1) % NS;
+                        if (!wait(kv_full(sk), (c / NS) & 1)) break;
+                        if (own) {
+                            qk(sk, cols(j));
+                            if (j + 2 >= tiles) tc_commit(q_empty(t), one);
+                        }
+                        tc_commit(kv_empty(sk), one);
+                        if (!wait(kv_full(sv), ((c + 1) / NS) & 1)) break;
+                        if (own) {
+                            pv(sv, there(j), cols(j), j > 1);
+                            if (!alive) break;
+                            if (j + 2 >= tiles) tc_commit(o_full(t), one);
+                        }
+                        tc_commit(kv_empty(sv), one);
+                    }
+                    continue;
+                }
                 if (!wait(kv_full(c % NS), (c / NS) & 1)) break;
                 if (mine > 0) {
-                    ++uses;
                     qk(c % NS, cols(0));
                     if (mine == 1) tc_commit(q_empty(t), one);
                 }
@@ -657,39 +726,12 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                 for (int j = 0; j < tiles; ++j) {
                     const int sv = c % NS, sk = (c + 1) % NS;
                     if (!wait(kv_full(sv), (c / NS) & 1)) break;
-                    const uint32_t v = base + SH::OFF_KV + sv * SH::TILE;
-                    const int left = w.kv_end - (w.j0 + j) * PF_BN;
-                    if (PAGED && left < PF_BN) {
-                        // Slots behind the context hold anything: their weights are 0, their values made 0.
-                        for (int i = left * HALVES * 8 + lane; i < PF_BN * HALVES * 8; i += 32) {
-                            const int row = i / (HALVES * 8), col = i % (HALVES * 8);
-                            const uint32_t at =
-                                v + (row >> 3) * KV_GROUP + (col >> 3) * KV_HALF + (row & 7) * 128 + (col & 7) * 16;
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
                     const bool more = j + 1 < tiles;
                     if (more && !wait(kv_full(sk), ((c + 1) / NS) & 1)) break;
                     if (j < mine) {
-                        const uint32_t vd = desc_lo(v, KV_HALF);
-                        auto pv = [&](int i) {  // keys 16 i to 16 i + 15
-                            tc_mma_ta(o_at, s_at + i * 8, vd + i * 2 * KV_GROUP / 16, desc_hi(KV_GROUP), idesc_pv,
-                                      j > 0 || i > 0, one);
-                        };
-                        const int steps = cols(j) / 16;
-                        // The product starts on the first three quarters of the weights.
-                        if (!wait(p_most(t), weights & 1)) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int i = 0; i < 6; ++i)
-                            if (i < steps) pv(i);
-                        if (!wait(p_full(t), weights & 1)) break;
-                        tc_fence_after();
-                        if (steps > 6) pv(6);
-                        if (steps > 7) pv(7);
-                        ++weights;
+                        pv(sv, there(j), cols(j), j > 0);
+                        if (!alive) break;
+                        // The next scores follow in the same pipe: they replace weights that are read by then.
                         if (j + 1 < mine) {
                             qk(sk, cols(j + 1));
                             if (j + 2 == mine) tc_commit(q_empty(t), one);
@@ -710,22 +752,22 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SH::REGS_SOFTMAX));
         // ---- softmax: a thread for each row ----
         const int t = warp >> 2, quarter = warp & 3;
-        const int r = t * PF_BM + quarter * 32 + lane;  // row of the item
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_addr = lanes + SH::S_COL + t * 128, o_addr = lanes + SH::O_COL + t * D;
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
         Item it;
-        int scores = 0, results = 0;  // tiles of scores taken, accumulators read
+        int scores = 0, results0 = 0, results1 = 0, pairs = 0;  // tiles of scores taken, accumulators, items in halves
         for (int nth = 0; alive && next_item(nth, it); ++nth) {
-            const Walk<NQ> w = walk_of<NQ>(it, tm, p.split_tiles);
-            const int mine = t == 0 ? w.count[0] : w.count[NQ - 1];
-            const int tok = it.tok0 + r / group, head = it.kvh * group + r % group;
+            const Walk w = walk_of(it, tm, p.split_tiles, PAGED);
+            const int mine = t == 0 ? w.count[0] : w.count[1];
+            const int r = quarter * 32 + lane, tok0 = it.tok0 + (w.halves ? 0 : t * tm);  // row of the tile
+            const int tok = tok0 + r / group, head = it.kvh * group + r % group;
             const bool valid = tok < it.n;
             const int visible = valid ? max(w.first + tok + 1, 0) : 0;
             // Keys that all of the warp's rows see, and that any does.
-            const int clear = max(w.first + it.tok0 + (r - lane) / group + 1, 0);
-            const int seen = max(w.first + min(it.tok0 + (r - lane + 31) / group, it.n - 1) + 1, 0);
+            const int clear = max(w.first + tok0 + (r - lane) / group + 1, 0);
+            const int seen = max(w.first + min(tok0 + (r - lane + 31) / group, it.n - 1) + 1, 0);
             float m = -INFINITY, l = 0.f;  // m: what the weights are relative to, unscaled
             for (int j = 0; j < mine; ++j) {
                 if (!wait(s_full(t), scores & 1)) break;
@@ -737,7 +779,7 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
                 tc_landed(x[0]);
 #pragma unroll
                 for (int c = 1; c < 4; ++c) tc_pin(x[c]);
-                const int key0 = (w.j0 + j) * PF_BN;
+                const int key0 = (w.j0 + (w.halves ? 2 * j + t : j)) * PF_BN;
                 const bool masked = key0 + PF_BN > clear;
                 if (masked) {
                     const int left = visible - key0;
@@ -823,28 +865,62 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
             // ---- the item's rows ----
             const int lo = w.j0 * PF_BN, hi = min(visible, w.j1 * PF_BN);  // keys the row has seen here
             const bool some = hi > lo;
-            const float inv = some ? (it.parts > 1 ? 1.f : 1.f / l) : 0.f;
+            float f0 = 1.f, f1 = 0.f;  // what the two tiles' results are multiplied by
+            if (w.halves) {
+                float2 *swap = reinterpret_cast<float2 *>(smem + SH::OFF_SWAP) + r;
+                if (t == 1) {
+                    *swap = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pair_full);
+                    if (!wait(pair_empty, pairs & 1)) break;
+                    ++pairs;
+                    ++results0;
+                    ++results1;
+                    continue;
+                }
+                if (!wait(pair_full, pairs & 1) || !wait(o_full(1), results1 & 1)) break;
+                ++pairs;
+                const float2 other = *swap;
+                const float top = fmaxf(m, other.x);
+                f0 = m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
+                f1 = other.x == -INFINITY ? 0.f : ex2((other.x - top) * p.scale_log2);
+                l = l * f0 + other.y * f1;
+                m = top;
+            }
+            if (it.parts == 1) {
+                const float inv = 1.f / l;
+                f0 *= inv;
+                f1 *= inv;
+            }
             bool again = some && !(l > 0.f && l < INFINITY);
             if (mine > 0) {
-                if (!wait(o_full(t), results & 1)) break;
-                ++results;
+                if (!wait(o_full(t), (t == 0 ? results0 : results1) & 1)) break;
                 tc_fence_after();
             }
+            results0 += w.count[0] > 0;
+            results1 += w.count[1] > 0;
             const size_t at = (size_t)(it.row0 + tok) * p.num_heads + head;
             const size_t part_at = (size_t)it.part * p.num_tokens * p.num_heads + at;
             float nan = 0.f;
+            const uint32_t other_addr = w.halves ? o_addr + D : o_addr;  // not in halves: f1 is 0
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = 0; c < D && mine > 0; c += 32) {
                 float o[32];
-                if (mine > 0) {
-                    tc_ld32(o_addr + c, o);
+                tc_ld32(o_addr + c, o);
+                if constexpr (PAGED) {
+                    float other[32];
+                    tc_ld32(other_addr + c, other);
                     tc_landed(o);
+                    tc_pin(other);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = fmaf(other[i], f1, o[i] * f0);
+                } else {
+                    tc_landed(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= f0;
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    o[i] = some ? o[i] * inv : 0.f;
-                    nan = fmaf(o[i], 0.f, nan);
-                }
+                for (int i = 0; i < 32; ++i) nan = fmaf(o[i], 0.f, nan);
                 __syncwarp();
                 if (!valid) {
                     // rows of no token: nothing to store
@@ -871,9 +947,19 @@ __global__ void __launch_bounds__(PrefillShape<D, NQ>::THREADS, NQ == 2 ? 1 : 2)
             }
             if (PAGED && it.parts > 1 && valid)
                 p.part_ml[part_at] = make_float2(some ? m * p.scale_log2 : -INFINITY, some ? l : 0.f);
-            again = again || !(nan == 0.f);
+            if (valid && !some) {  // a row that sees nothing here: zeros, over what is in its place
+                const uint32_t none[8] = {};
+                if (PAGED && it.parts > 1) {
+                    for (int c = 0; c < D; c += 8) store_32b(p.part_acc + part_at * D + c, none);
+                } else {
+                    uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + at * D);
+                    for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0, 0, 0, 0);
+                }
+            }
+            again = again || (some && !(nan == 0.f));
             tc_fence_before();
             __syncwarp();
+            if (w.halves && lane == 0) mbar_arrive(pair_empty);
             for (unsigned rows = __ballot_sync(FULL_MASK, again); rows; rows &= rows - 1) {
                 const int src = __ffs(rows) - 1;
                 const int row = it.row0 + __shfl_sync(FULL_MASK, tok, src), h = __shfl_sync(FULL_MASK, head, src);
