@@ -459,7 +459,7 @@ PA_API pa_status pa_reshape_and_cache(const void *k, const void *v, void *k_pool
  * All arrays are device memory: int32, 4-byte aligned, slot_mapping int64,
  * 8-byte aligned. free_blocks has num_blocks entries. num_seqs <= 8192,
  * block_size in {16, 32, 64}; max_tokens, num_blocks and the tokens of a table row
- * are below 2^30 - 1. One launch, no workspace.
+ * are below 2^30 - 1. One launch, or two for many tokens; no workspace.
  */
 PA_API pa_status pa_assign_slots(int32_t *block_tables, int32_t *free_blocks, int32_t *context_lens_out,
                                  int32_t *num_free_out, int64_t *slot_mapping, int32_t *positions,

@@ -4,9 +4,9 @@
 // Every quantity is a prefix sum over the requests: new tokens (the packed
 // boundaries), blocks taken and blocks given back (places on the free stack).
 // The requests are few (thousands) and the outputs may be many (a slot and a
-// position for each new token), so each CTA of one cluster sums over all the
-// requests by itself, and the CTAs share the output rows; an output finds its
-// request by a binary search in the sums, held in shared memory.
+// position for each new token), so every CTA sums over all the requests by
+// itself, and the CTAs share the outputs; an output finds its request by a
+// binary search in the sums, held in shared memory.
 //
 // The free stack after the ended requests' pushes is free_blocks[0 .. nf)
 // followed by the released ids, so it is never materialised: the i-th block
@@ -15,9 +15,15 @@
 // written. No entry that is read is written (released and tail entries lie
 // below a request's block count, new ones at or above it; the free list is
 // read below nf and written from nf on), except where the caller passes the
-// lengths in place: those are written after a cluster barrier behind the
-// last read.
-#include <cooperative_groups.h>
+// lengths in place: a single CTA writes those behind a barrier after its last
+// read; where there are more, a second launch of one CTA sums again and writes
+// them.
+//
+// Latency bounds it: a decode step's 256 tokens are one CTA and one launch
+// (3.7 us in a graph, most of it the launch); 150,000 slots of 192 prompts took
+// 31 us on a cluster of 8 CTAs, whose barrier let it write the lengths too, and
+// take 9.5 with a CTA an SM and the second launch.
+#include <atomic>
 
 #define PA_ERROR_WORD_ELSEWHERE
 #include "pa_common.cuh"
@@ -25,18 +31,17 @@
 
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int ASSIGN_THREADS = 1024;
 constexpr int ASSIGN_MAX_SEQS = 8192;
-constexpr int ASSIGN_MAX_CLUSTER = 8;
+
+// What a launch writes: the outputs, the lengths and the size of the free list.
+constexpr int ASSIGN_OUTPUTS = 1, ASSIGN_LENGTHS = 2;
 constexpr int SUM_CAP = (1 << 30) - 1;  // prefix sums saturate here: above every valid total, and two of them fit an int
 
 struct AssignParams {
     int32_t *block_tables, *free_blocks, *context_lens_out, *num_free_out, *positions, *cu_seqlens;
     int64_t *slot_mapping;
     const int32_t *context_lens, *num_free, *new_lens;
-    int num_seqs, width, block_size, num_blocks, max_tokens;
+    int num_seqs, width, block_size, num_blocks, max_tokens, writes;
     unsigned int *errors;
 };
 
@@ -55,15 +60,16 @@ __device__ __forceinline__ int find_seq(const int *off, int n, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(ASSIGN_THREADS) pa_assign_kernel(AssignParams p) {
+template <int ASSIGN_THREADS>
+__global__ void __launch_bounds__(ASSIGN_THREADS) pa_assign_kernel(const __grid_constant__ AssignParams p) {
     extern __shared__ int smem[];
     const int B = p.num_seqs, bs = p.block_size;
     int *tok = smem, *take = tok + B + 1, *back = take + B + 1, *ctx = back + B + 1;
-    __shared__ int warp_sum[3][32];
+    constexpr int NW = ASSIGN_THREADS / 32;
+    __shared__ int warp_sum[3][NW];
     __shared__ int carry[3];
     __shared__ unsigned bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    cg::cluster_group cluster = cg::this_cluster();
     if (tid < 3) carry[tid] = 0;
     if (tid == 0) bad = 0u;
     const int nf = *p.num_free;
@@ -104,13 +110,13 @@ __global__ void __launch_bounds__(ASSIGN_THREADS) pa_assign_kernel(AssignParams 
             for (int k = 0; k < 3; ++k) warp_sum[k][warp] = v[k];
         __syncthreads();
         if (warp < 3) {
-            int w = warp_sum[warp][lane];
+            int w = lane < NW ? warp_sum[warp][lane] : 0;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int up = __shfl_up_sync(pa::FULL_MASK, w, off);
                 if (lane >= off) w = sat_add(w, up);
             }
-            warp_sum[warp][lane] = w;
+            if (lane < NW) warp_sum[warp][lane] = w;
         }
         __syncthreads();
 #pragma unroll
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(ASSIGN_THREADS) pa_assign_kernel(AssignParams 
             back[s] = v[2] - mine[2];
         }
         __syncthreads();
-        if (tid < 3) carry[tid] = sat_add(carry[tid], warp_sum[tid][31]);
+        if (tid < 3) carry[tid] = sat_add(carry[tid], warp_sum[tid][NW - 1]);
         __syncthreads();
     }
     const int new_tokens = carry[0], taken = carry[1], given = carry[2];
@@ -137,12 +143,12 @@ __global__ void __launch_bounds__(ASSIGN_THREADS) pa_assign_kernel(AssignParams 
         if (new_tokens > p.max_tokens) why |= PA_DEVERR_TOKENS;
         if (nf < 0 || nf > p.num_blocks || given > p.num_blocks - nf || taken > nf + given) why |= PA_DEVERR_BLOCKS;
         bad = why;
-        if (why && cluster.block_rank() == 0) atomicOr(p.errors, why);
+        if (why && blockIdx.x == 0) atomicOr(p.errors, why);
     }
     __syncthreads();
     const bool ok = bad == 0u;
-    const int worker = (int)cluster.block_rank() * ASSIGN_THREADS + tid;
-    const int workers = (int)cluster.num_blocks() * ASSIGN_THREADS;
+    const int worker = (int)blockIdx.x * ASSIGN_THREADS + tid;
+    const int workers = (int)gridDim.x * ASSIGN_THREADS;
     bool bad_id = false;
 
     // Entry i of the stack of free blocks: the free list, then the released blocks.
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(ASSIGN_THREADS) pa_assign_kernel(AssignParams 
         bad_id |= (unsigned)id >= (unsigned)p.num_blocks;
         return id;
     };
-    if (ok) {
+    if (ok && (p.writes & ASSIGN_OUTPUTS)) {
         const int top = nf + given, left = top - taken;
         for (int i = worker; i < taken; i += workers) {
             const int s = find_seq(take, B, i);
@@ -185,21 +191,44 @@ __global__ void __launch_bounds__(ASSIGN_THREADS) pa_assign_kernel(AssignParams 
             p.positions[t] = pos;
             p.slot_mapping[t] = slot;
         }
-    } else {
+    } else if (p.writes & ASSIGN_OUTPUTS) {
         for (int t = worker; t < p.max_tokens; t += workers) {
             p.positions[t] = -1;
             p.slot_mapping[t] = -1;
         }
     }
     if (bad_id) atomicOr(p.errors, PA_DEVERR_BLOCK_ID);
-    for (int s = worker; s <= B; s += workers) p.cu_seqlens[s] = ok ? tok[s] : 0;
-    // Every CTA has read the lengths: they may now be replaced in place.
-    cluster.sync();
-    for (int s = worker; s < B; s += workers) {
-        const int n = p.new_lens[s];
-        p.context_lens_out[s] = !ok ? p.context_lens[s] : n < 0 ? 0 : ctx[s] + n;
+    if (p.writes & ASSIGN_OUTPUTS)
+        for (int s = worker; s <= B; s += workers) p.cu_seqlens[s] = ok ? tok[s] : 0;
+    if (p.writes & ASSIGN_LENGTHS) {  // one CTA: it has read the lengths, they may now be replaced in place
+        __syncthreads();
+        for (int s = tid; s < B; s += ASSIGN_THREADS) {
+            const int n = p.new_lens[s];
+            p.context_lens_out[s] = !ok ? p.context_lens[s] : n < 0 ? 0 : ctx[s] + n;
+        }
+        if (tid == 0) *p.num_free_out = ok ? nf + given - taken : nf;
     }
-    if (worker == 0) *p.num_free_out = ok ? nf + given - taken : nf;
+}
+
+template <int THREADS>
+pa_status launch(const AssignParams &p, int ctas, cudaStream_t stream) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> done[kMaxDevices];
+    int dev, sms;
+    const pa_status st = pa_internal_device(&dev, &sms);
+    if (st != PA_OK) return st;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(pa_assign_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (4 * ASSIGN_MAX_SEQS + 3) * (int)sizeof(int));
+        if (e != cudaSuccess) return pa_host::cuda_fail(e, "cudaFuncSetAttribute");
+        done[dev].store(true, std::memory_order_release);
+    }
+    if (ctas > sms) ctas = sms;
+    pa_assign_kernel<THREADS><<<ctas, THREADS, (4 * p.num_seqs + 3) * sizeof(int), stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return pa_host::cuda_fail(e, "pa_assign_slots launch");
+    pa_internal_count_launch();
+    return PA_OK;
 }
 
 }  // namespace
@@ -227,29 +256,20 @@ extern "C" pa_status pa_assign_slots(int32_t *block_tables, int32_t *free_blocks
         return fail(PA_ERR_INVALID, "misaligned pointer (4 B int32 arrays, 8 B slot_mapping)");
     AssignParams p{block_tables, free_blocks,  context_lens_out, num_free_out, positions,
                    cu_seqlens,   slot_mapping, context_lens,     num_free,     new_lens,
-                   num_seqs,     max_blocks_per_seq, block_size, num_blocks,   max_tokens, nullptr};
-    pa_status st = pa_internal_error_word(&p.errors);
+                   num_seqs,     max_blocks_per_seq, block_size, num_blocks,   max_tokens,
+                   ASSIGN_OUTPUTS | ASSIGN_LENGTHS, nullptr};
+    const pa_status st = pa_internal_error_word(&p.errors);
     if (st != PA_OK) return st;
-    const int smem = (4 * num_seqs + 3) * (int)sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(pa_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (4 * ASSIGN_MAX_SEQS + 3) * (int)sizeof(int));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    int ctas = 1;
-    while (ctas < ASSIGN_MAX_CLUSTER && ctas * ASSIGN_THREADS * 4 < max_tokens) ctas *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(ASSIGN_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, pa_assign_kernel, p);
-    if (e != cudaSuccess) return cuda_fail(e, "pa_assign_slots launch");
-    pa_internal_count_launch();
-    return PA_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // One CTA where the outputs are few, a small one where the requests are too (us in a
+    // graph, 256 threads / 1024 threads / a CTA an SM and the second launch: 256 requests of
+    // one token 3.7 / 4.2 / 6.6; 64 of 16 6.2 / 4.8 / 7.4; 64 of 64 14.2 / 7.9 / 7.6; 64 of 256
+    // 49.9 / 19.2 / 7.6; 8192 of one 66 / 27 / 29).
+    if (max_tokens <= 512 && num_seqs <= 256) return launch<256>(p, 1, s);
+    if (max_tokens <= 4096 || max_tokens <= num_seqs) return launch<1024>(p, 1, s);
+    p.writes = ASSIGN_OUTPUTS;
+    const pa_status out = launch<1024>(p, (max_tokens + 1023) / 1024, s);
+    if (out != PA_OK) return out;
+    p.writes = ASSIGN_LENGTHS;
+    return launch<1024>(p, 1, s);
 }

@@ -2,7 +2,8 @@
 // k and of v into the paged cache (include/pa.h).
 //
 // One pass over the rows: every element is read once and written once (k twice
-// where k_out is wanted too), so the copy bandwidth bounds it. A thread handles
+// where k_out is wanted too), so the copy bandwidth bounds it (8192 tokens of 96
+// heads of 128: 80 us, 5.9 TB/s). A thread handles
 // two 16-byte vectors at a time whose elements pair up under the rotation: in
 // the half layout the vectors at 8u and rot_dim/2 + 8u, interleaved the two
 // neighbours at 16u; both use frequencies 8u .. 8u+7. The angles belong to the
@@ -19,7 +20,8 @@
 namespace {
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_MAX_TOKENS = 4;  // tokens of a CTA at a time
+constexpr int ROPE_W = 3;            // units a thread has in flight
+constexpr int ROPE_MAX_TOKENS = 16;  // tokens of a CTA
 
 struct RopeParams {
     void *q_out, *k_out;
@@ -32,7 +34,7 @@ struct RopeParams {
     long long num_slots;
     int q_stride, k_stride, v_stride;
     float mscale;
-    int tokens_per_cta;
+    int lanes_log2, tokens_per_cta;  // threads of a token, tokens of a CTA
     unsigned int *errors;
 };
 
@@ -66,15 +68,16 @@ __device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float2 *cs) {
     b = make_uint4(E::pack(y[0], y[1]), E::pack(y[2], y[3]), E::pack(y[4], y[5]), E::pack(y[6], y[7]));
 }
 
-template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(ROPE_THREADS) pa_rope_kernel(RopeParams p) {
+// D: head size, W: units (pairs of vectors) a thread has in flight.
+template <typename T, bool INTERLEAVED, int D, int W>
+__global__ void __launch_bounds__(ROPE_THREADS) pa_rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ float2 cs[ROPE_MAX_TOKENS][64];
-    const int D = p.head_dim, rot = p.rot_dim, half = rot / 2;
-    const int units = D / 16;  // two-vector units of a head
-    const int H = p.num_heads, Hkv = p.num_kv_heads, heads = H + 2 * Hkv;
+    constexpr int UNITS = D / 16;  // units of a head
+    const int rot = p.rot_dim, half = rot / 2;
+    const int H = p.num_heads, Hkv = p.num_kv_heads;
     const int t0 = blockIdx.x * p.tokens_per_cta;
     const int nt = min(p.tokens_per_cta, p.num_tokens - t0);
-    for (int i = threadIdx.x; i < nt * half; i += ROPE_THREADS) {
+    for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
         const int t = i / half, f = i - t * half;
         const double turns = (double)p.positions[t0 + t] * (p.inv_freq[f] * 0.15915494309189533577);
         float s, c;
@@ -82,51 +85,71 @@ __global__ void __launch_bounds__(ROPE_THREADS) pa_rope_kernel(RopeParams p) {
         cs[t][f] = make_float2(c * p.mscale, s * p.mscale);
     }
     __syncthreads();
-    const int per_token = heads * units;
-    for (int i = threadIdx.x; i < nt * per_token; i += ROPE_THREADS) {
-        const int tl = i / per_token, r = i - tl * per_token;
-        const int head = r / units, u = r - head * units;
+    const int per_token = (H + (p.v_pool ? 2 : 1) * Hkv) * UNITS;
+    const int lanes = 1 << p.lanes_log2, lane = threadIdx.x & (lanes - 1);
+    for (int tl = threadIdx.x >> p.lanes_log2; tl < nt; tl += blockDim.x >> p.lanes_log2) {
         const int t = t0 + tl;
         if (p.positions[t] < 0) continue;
-        const bool is_q = head < H, is_v = head >= H + Hkv;
-        if (is_v && !p.v_pool) continue;
-        const int h = is_q ? head : is_v ? head - H - Hkv : head - H;
-        const T *src = is_q   ? static_cast<const T *>(p.q) + (size_t)t * p.q_stride
-                       : is_v ? static_cast<const T *>(p.v) + (size_t)t * p.v_stride
-                              : static_cast<const T *>(p.k) + (size_t)t * p.k_stride;
-        src += (size_t)h * D;
-        const bool turn = !is_v && 16 * u < rot;
-        const int e0 = turn && !INTERLEAVED ? 8 * u : 16 * u;
-        const int e1 = turn && !INTERLEAVED ? half + 8 * u : 16 * u + 8;
-        uint4 a = *reinterpret_cast<const uint4 *>(src + e0);
-        uint4 b = *reinterpret_cast<const uint4 *>(src + e1);
-        if (turn) rotate<T, INTERLEAVED>(a, b, &cs[tl][8 * u]);
-        if (is_q) {
-            T *dst = static_cast<T *>(p.q_out) + ((size_t)t * H + h) * D;
-            *reinterpret_cast<uint4 *>(dst + e0) = a;
-            *reinterpret_cast<uint4 *>(dst + e1) = b;
-            continue;
-        }
-        if (!is_v && p.k_out) {
-            T *dst = static_cast<T *>(p.k_out) + ((size_t)t * Hkv + h) * D;
-            *reinterpret_cast<uint4 *>(dst + e0) = a;
-            *reinterpret_cast<uint4 *>(dst + e1) = b;
-        }
+        int64_t at = -1;  // first element of the token's slot in head 0
         if (p.k_pool) {
             const int64_t slot = p.slot_mapping[t];
-            if (slot < 0) continue;
             if (slot >= p.num_slots) {
-                atomicOr(p.errors, PA_DEVERR_SLOT);
-                continue;
+                if (lane == 0) atomicOr(p.errors, PA_DEVERR_SLOT);
+            } else if (slot >= 0) {
+                const int64_t blk = slot / p.block_size;
+                at = (blk * Hkv * p.block_size + (slot - blk * p.block_size)) * D;
             }
-            const int64_t blk = slot / p.block_size;
-            const int off = (int)(slot - blk * p.block_size);
-            T *dst = static_cast<T *>(is_v ? p.v_pool : p.k_pool) +
-                     (((size_t)blk * Hkv + h) * p.block_size + off) * D;
-            *reinterpret_cast<uint4 *>(dst + e0) = a;
-            *reinterpret_cast<uint4 *>(dst + e1) = b;
+        }
+        const T *q = static_cast<const T *>(p.q) + (size_t)t * p.q_stride;
+        const T *k = static_cast<const T *>(p.k) + (size_t)t * p.k_stride;
+        const T *v = static_cast<const T *>(p.v) + (size_t)t * p.v_stride;
+        for (int r0 = lane; r0 < per_token; r0 += lanes * W) {
+            uint4 a[W], b[W];
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const int r = r0 + w * lanes, head = r / UNITS, u = r % UNITS;
+                if (r >= per_token) break;
+                const bool is_v = head >= H + Hkv, turn = !is_v && 16 * u < rot;
+                const T *src = head < H ? q + (size_t)head * D : is_v ? v + (size_t)(head - H - Hkv) * D : k + (size_t)(head - H) * D;
+                a[w] = *reinterpret_cast<const uint4 *>(src + (turn && !INTERLEAVED ? 8 * u : 16 * u));
+                b[w] = *reinterpret_cast<const uint4 *>(src + (turn && !INTERLEAVED ? half + 8 * u : 16 * u + 8));
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const int r = r0 + w * lanes, head = r / UNITS, u = r % UNITS;
+                if (r >= per_token) break;
+                const bool is_q = head < H, is_v = head >= H + Hkv, turn = !is_v && 16 * u < rot;
+                const int e0 = turn && !INTERLEAVED ? 8 * u : 16 * u;
+                const int e1 = turn && !INTERLEAVED ? half + 8 * u : 16 * u + 8;
+                if (turn) rotate<T, INTERLEAVED>(a[w], b[w], &cs[tl][8 * u]);
+                if (is_q) {
+                    T *dst = static_cast<T *>(p.q_out) + ((size_t)t * H + head) * D;
+                    *reinterpret_cast<uint4 *>(dst + e0) = a[w];
+                    *reinterpret_cast<uint4 *>(dst + e1) = b[w];
+                    continue;
+                }
+                const int h = is_v ? head - H - Hkv : head - H;
+                if (!is_v && p.k_out) {
+                    T *dst = static_cast<T *>(p.k_out) + ((size_t)t * Hkv + h) * D;
+                    *reinterpret_cast<uint4 *>(dst + e0) = a[w];
+                    *reinterpret_cast<uint4 *>(dst + e1) = b[w];
+                }
+                if (at >= 0) {
+                    T *dst = static_cast<T *>(is_v ? p.v_pool : p.k_pool) + at + (int64_t)h * p.block_size * D;
+                    *reinterpret_cast<uint4 *>(dst + e0) = a[w];
+                    *reinterpret_cast<uint4 *>(dst + e1) = b[w];
+                }
+            }
         }
     }
+}
+
+template <typename T, bool INTERLEAVED>
+void launch(const RopeParams &p, unsigned grid, unsigned threads, cudaStream_t s) {
+    if (p.head_dim == 128)
+        pa_rope_kernel<T, INTERLEAVED, 128, ROPE_W><<<grid, threads, 0, s>>>(p);
+    else
+        pa_rope_kernel<T, INTERLEAVED, 64, ROPE_W><<<grid, threads, 0, s>>>(p);
 }
 
 }  // namespace
@@ -166,22 +189,29 @@ extern "C" pa_status pa_rope_and_cache(void *q_out, void *k_out, const void *q, 
         return fail(PA_ERR_INVALID, "in place needs a contiguous input");
     RopeParams p{q_out, k_out, q, k, v, k_pool, v_pool, positions, slot_mapping, static_cast<const double *>(inv_freq),
                  num_tokens, num_heads, num_kv_heads, head_dim, rot_dim, cache ? block_size : 16,
-                 cache ? (long long)num_blocks * block_size : 0, q_stride, k_stride, v_stride, mscale, 1, nullptr};
+                 cache ? (long long)num_blocks * block_size : 0, q_stride, k_stride, v_stride, mscale, 5, 1, nullptr};
     int dev, sms;
     pa_status st = pa_internal_device(&dev, &sms);
     if (st != PA_OK) return st;
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
-    // Few tokens: one a CTA, so that they spread over the SMs. Many: four, whose
-    // angles (up to 64 each) occupy all the CTA's threads at once.
-    p.tokens_per_cta = num_tokens >= sms * ROPE_MAX_TOKENS * 4 ? ROPE_MAX_TOKENS : 1;
+    // A token has the threads that its units fill with ROPE_W each in flight, a CTA as
+    // many tokens at a time as fit, two times where the tokens are many; fewer where the
+    // SMs would not have two CTAs each. (2049 tokens of 24 heads of 64: 5.9 us, 11.8 with a
+    // whole CTA a token; 8192 tokens of 96 heads of 128: 80 us with two tokens a CTA, 83 with
+    // one or four.)
+    const int units = (num_heads + (cache ? 2 : 1) * num_kv_heads) * (head_dim / 16);
+    p.lanes_log2 = 5;
+    while ((1 << p.lanes_log2) < ROPE_THREADS && (ROPE_W << p.lanes_log2) < units) ++p.lanes_log2;
+    int at_once = ROPE_THREADS >> p.lanes_log2;
+    while (at_once > 1 && num_tokens / at_once < 2 * sms) at_once /= 2;
+    const unsigned threads = (unsigned)at_once << p.lanes_log2;
+    p.tokens_per_cta = num_tokens / (2 * at_once) < 8 * sms ? at_once : 2 * at_once;
     const unsigned grid = (unsigned)((num_tokens + (long long)p.tokens_per_cta - 1) / p.tokens_per_cta);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == PA_F16)
-        interleaved ? pa_rope_kernel<__half, true><<<grid, ROPE_THREADS, 0, s>>>(p)
-                    : pa_rope_kernel<__half, false><<<grid, ROPE_THREADS, 0, s>>>(p);
+        interleaved ? launch<__half, true>(p, grid, threads, s) : launch<__half, false>(p, grid, threads, s);
     else
-        interleaved ? pa_rope_kernel<__nv_bfloat16, true><<<grid, ROPE_THREADS, 0, s>>>(p)
-                    : pa_rope_kernel<__nv_bfloat16, false><<<grid, ROPE_THREADS, 0, s>>>(p);
+        interleaved ? launch<__nv_bfloat16, true>(p, grid, threads, s) : launch<__nv_bfloat16, false>(p, grid, threads, s);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "pa_rope_and_cache launch");
     pa_internal_count_launch();
