@@ -101,9 +101,17 @@ pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, PAGED ? "pa_prefill_paged launch" : "pa_prefill launch");
     pa_internal_count_launch();
     if (PAGED && max_parts > 1) {
-        const long long rows = (long long)p.num_tokens * p.num_heads;
-        pa::pa_prefill_join_kernel<D, T><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
-        e = cudaGetLastError();
+        // Started early, it waits for the attention launch behind its own look-ups.
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(p.num_tokens * p.num_heads));
+        cfg.blockDim = dim3(128);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, pa::pa_prefill_join_kernel<D, T>, p);
         if (e != cudaSuccess) return cuda_fail(e, "pa_prefill_paged launch");
         pa_internal_count_launch();
     }
@@ -127,6 +135,7 @@ struct Cut {
 
 Cut cut_of(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int max_keys, int sms) {
     const long long rows = (long long)num_tokens * (num_heads / num_kv_heads);
+    if ((long long)num_tokens * num_heads >= (1ll << 31)) return Cut{0, 1};
     const long long items =
         std::max<long long>(std::min(num_seqs, num_tokens), ceil_div(rows, pa::PF_NQ * pa::PF_BM)) * num_kv_heads;
     const int tiles = (int)ceil_div(max_keys, pa::PF_BN);

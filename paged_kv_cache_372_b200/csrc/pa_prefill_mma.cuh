@@ -41,7 +41,10 @@ namespace pa {
 constexpr int PF_NQ = 2;    // tiles of rows of an item
 constexpr int PF_BM = 128;  // rows of a tile
 constexpr int PF_BN = 128;  // keys of a tile
-constexpr int PF_POLY = 4;  // of 16 pairs of exponentials, those on the FMA units
+// Of 16 pairs of exponentials, those on the FMA units (8192 tokens, us, 2 / 4 / 6: head size
+// 64 bf16 350 / 374 / 364, 128 fp16 416 / 404 / 414).
+template <int D>
+constexpr int PF_POLY = D == 64 ? 2 : 4;
 constexpr uint64_t PF_WAIT_NS = 4000000000ull;
 
 template <int D>
@@ -819,7 +822,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 y = fma2(make_float2(x[c][2 * i], x[c][2 * i + 1]), scale2, ref2);
-                        if (i * PF_POLY % 16 < PF_POLY)
+                        if (i * PF_POLY<D> % 16 < PF_POLY<D>)
                             y = ex2_fma<T>(y);
                         else
                             y = make_float2(ex2(y.x), ex2(y.y));
@@ -901,7 +904,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             results1 += w.count[1] > 0;
             const size_t at = (size_t)(it.row0 + tok) * p.num_heads + head;
             const size_t part_at = (size_t)it.part * p.num_tokens * p.num_heads + at;
-            float nan = 0.f;
+            float2 nan[4] = {};  // 0 as long as all that goes in is finite
             const uint32_t other_addr = w.halves ? o_addr + D : o_addr;  // not in halves: f1 is 0
 #pragma unroll 1
             for (int c = 0; c < D && mine > 0; c += 32) {
@@ -920,7 +923,10 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                     for (int i = 0; i < 32; ++i) o[i] *= f0;
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) nan = fmaf(o[i], 0.f, nan);
+                for (int i = 0; i < 32; i += 2) {
+                    float2 &at = nan[(i >> 1) & 3];
+                    at = fma2(make_float2(o[i], o[i + 1]), make_float2(0.f, 0.f), at);
+                }
                 __syncwarp();
                 if (!valid) {
                     // rows of no token: nothing to store
@@ -956,7 +962,8 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                     for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0, 0, 0, 0);
                 }
             }
-            again = again || (some && !(nan == 0.f));
+            const float2 any = add2(add2(nan[0], nan[1]), add2(nan[2], nan[3]));
+            again = again || (some && !(any.x + any.y == 0.f));
             tc_fence_before();
             __syncwarp();
             if (w.halves && lane == 0) mbar_arrive(pair_empty);
@@ -976,16 +983,18 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
     }
 }
 
-// Joins the parts of split contexts: a warp for each (token, head) row.
+// Joins the parts of split contexts: four warps for each (token, head) row, a
+// quarter of the parts each.
 //   out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i
 template <int D, typename T>
-__global__ void __launch_bounds__(256) pa_prefill_join_kernel(const __grid_constant__ PrefillParams p) {
+__global__ void __launch_bounds__(128) pa_prefill_join_kernel(const __grid_constant__ PrefillParams p) {
     constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (item >= (long long)p.num_tokens * p.num_heads) return;
-    const int row = (int)(item / p.num_heads);
-    int lo = 0, hi = p.num_seqs;  // the last sequence that starts at or before the row
+    __shared__ float acc_of[4][D];
+    __shared__ float2 ml_of[4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int item = blockIdx.x, row = item / p.num_heads;
+    // The last sequence that starts at or before the row.
+    int lo = 0, hi = p.num_seqs;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (p.cu_seqlens[mid] <= row)
@@ -995,19 +1004,15 @@ __global__ void __launch_bounds__(256) pa_prefill_join_kernel(const __grid_const
     }
     unsigned bad = 0;
     const SeqRange r = seq_range<true>(p, lo, bad);
-    if (row < r.row0 || row >= r.row0 + r.n) return;
     const int parts = parts_of(r.keys, p.split_tiles);
-    if (parts == 1) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention launch before this one is done
+    if (row < r.row0 || row >= r.row0 + r.n || parts == 1) return;
     const size_t stride = (size_t)p.num_tokens * p.num_heads;
     float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[i * stride + item].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
+    for (int i = warp; i < parts; i += 4) {
         const float2 ml = p.part_ml[i * stride + item];
         const float *a = p.part_acc + (i * stride + item) * D + lane * E;
         float x[E];
@@ -1018,16 +1023,35 @@ __global__ void __launch_bounds__(256) pa_prefill_join_kernel(const __grid_const
             const float2 v = *reinterpret_cast<const float2 *>(a);
             x[0] = v.x, x[1] = v.y;
         }
-        const float f = exp2f(ml.x - ref);
-        l = fmaf(ml.y, f, l);
+        const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+        const float f0 = exp2f(m - ref), f1 = exp2f(ml.x - ref);
+        m = top;
+        l = l * f0 + ml.y * f1;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], f, acc[e]);
+        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + x[e] * f1;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc_of[warp][lane * E + e] = acc[e];
+    if (lane == 0) ml_of[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp) return;
+    const float top = fmaxf(fmaxf(ml_of[0].x, ml_of[1].x), fmaxf(ml_of[2].x, ml_of[3].x));
+    const float ref = top == -INFINITY ? 0.f : top;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f = exp2f(ml_of[i].x - ref);
+        l = fmaf(ml_of[i].y, f, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(acc_of[i][lane * E + e], f, acc[e]);
     }
     const bool some = r.keys - r.n + (row - r.row0) + 1 > 0;
     const float inv = some ? 1.f / l : 0.f;
     uint32_t *op = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + (size_t)item * D) + lane * (E / 2);
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) op[e] = Elem<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    for (int e = 0; e < E / 2; ++e) op[e] = Elem<T>::pack(some ? acc[2 * e] * inv : 0.f, some ? acc[2 * e + 1] * inv : 0.f);
 }
 
 }  // namespace pa
