@@ -523,7 +523,8 @@ PA_API pa_status pa_rope_and_cache(void *q_out, void *k_out, const void *q, cons
  * and behind the last one do not reach it.
  * q, k, v and their strides as in pa_rope_and_cache; out [num_tokens][num_heads]
  * [head_dim] contiguous, not overlapping an input. Heads, head_dim and
- * dtype as pa_decode. scale must be finite. No workspace; one launch.
+ * dtype as pa_decode; fewer than 2^27 tokens. scale must be finite (at most 2^127
+ * in magnitude). No workspace; one launch.
  */
 PA_API pa_status pa_prefill(void *out, const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
                             int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
@@ -541,6 +542,7 @@ PA_API pa_status pa_prefill(void *out, const void *q, const void *k, const void 
  * Pools, block_tables, context_lens and max_context_len as pa_decode (16-bit
  * cache); q, q_stride, cu_seqlens, out, scale and the treatment of other rows
  * as pa_prefill. Cache slots past a context are never read into a result.
+ * max_context_len is below 2^30, num_blocks * num_kv_heads below 2^31.
  *
  * Where the rows are too few to fill the device their contexts are split and
  * the parts merged by the log-sum-exp identity in a second launch.

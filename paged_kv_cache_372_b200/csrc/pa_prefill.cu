@@ -186,7 +186,8 @@ pa_status check_common(int num_seqs, int num_tokens, int num_heads, int num_kv_h
     if (num_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 heads");
     if (head_dim != 64 && head_dim != 128) return fail(PA_ERR_UNSUPPORTED, "head_dim %d", head_dim);
     if (num_tokens >= (1 << 27)) return fail(PA_ERR_UNSUPPORTED, "num_tokens must be below 2^27");
-    if (!(scale - scale == 0.f)) return fail(PA_ERR_INVALID, "scale must be finite");
+    if (!(scale - scale == 0.f) || fabsf(scale) > FLT_MAX / 2)
+        return fail(PA_ERR_INVALID, "scale must be finite and at most 2^127 in magnitude");
     return PA_OK;
 }
 
@@ -228,7 +229,7 @@ size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_hea
                                        int block_size, int max_context_len) {
     if (num_seqs < 0 || num_tokens < 0 || max_context_len < 0 || !heads_supported(num_heads, num_kv_heads) ||
         num_heads > 65535 || (head_dim != 64 && head_dim != 128) || !block_size_supported(block_size) ||
-        num_tokens >= (1 << 27))
+        num_tokens >= (1 << 27) || max_context_len >= (1 << 30))
         return 0;
     if (num_seqs == 0 || num_tokens == 0) return 256;
     int dev, sms;
@@ -250,6 +251,8 @@ pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const v
     pa_status st = check_common(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, scale, dtype);
     if (st != PA_OK) return st;
     if (!block_size_supported(block_size)) return fail(PA_ERR_UNSUPPORTED, "block_size %d", block_size);
+    if (max_context_len >= (1 << 30) || (long long)num_blocks * num_kv_heads >= (1ll << 31))
+        return fail(PA_ERR_UNSUPPORTED, "max_context_len must be below 2^30, num_blocks * num_kv_heads below 2^31");
     if (num_seqs == 0 || num_tokens == 0) return PA_OK;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !context_lens || !cu_seqlens || !workspace)
         return fail(PA_ERR_INVALID, "null pointer");
