@@ -45,8 +45,11 @@ constexpr int kMaxDevices = 64;
 
 // Contexts are split where there are fewer items than kSplitItems an SM (a paged
 // call of few rows), into parts of kSplitTiles key tiles at least; a part costs
-// about kPartTiles key tiles beside its own (its start and end, its partial result).
-constexpr long long kSplitItems = 6;
+// about kPartTiles key tiles beside its own (its start and end, its partial
+// result). Back to back, us at 3 / 6 items an SM: 512-token pieces of eight
+// 32768-token prompts 1969 (not split: 3.5 items an SM) / 1998 (two parts), 5-8
+// tokens over 4096-32768 110 / 113; at 24 the latter took 131.
+constexpr long long kSplitItems = 3;
 constexpr int kSplitTiles = 4, kPartTiles = 4;
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
