@@ -17,7 +17,7 @@
 // that finds the next work item. While the softmax of one tile of rows runs, the
 // other's products do: at head size 128 a tile needs 128 x 128 exponentials at
 // 16 a clock and 4 x 128^3 product operations at 8192 a clock, 1024 clocks
-// either way, so a quarter of the exponentials go to the FMA units (ex2_fma).
+// either way, so 4 or 5 of 16 exponentials go to the FMA units (ex2_fma).
 //
 // CTAs are persistent: a CTA that works on an item takes over the launch of the
 // next one that has not started (clusterlaunchcontrol) and its copies and first
@@ -50,10 +50,12 @@ namespace pa {
 constexpr int PF_NQ = 2;    // tiles of rows of an item
 constexpr int PF_BM = 128;  // rows of a tile
 constexpr int PF_BN = 128;  // keys of a tile
-// Of 16 pairs of exponentials, those on the FMA units (8192 tokens, us, 2 / 4 / 6: head size
-// 64 bf16 350 / 374 / 364, 128 fp16 416 / 404 / 414).
+// Of 16 pairs of exponentials, those on the FMA units. 8192 tokens, 32/8 heads of
+// 64, us at 0 / 2 / 4 / 6 / 8 pairs: bf16 350 / 385 / 340 / 345 / 367, fp16 352 / 374 /
+// 340 / 345 / 381; 16384 tokens, heads of 128, bf16, at 3 / 4 / 5 / 6: 1585 / 1510 / 1495 / 1493,
+// LLaMA-7B-shaped prompts, fp16, 199 / 192 / 190 / 195.
 template <int D>
-constexpr int PF_POLY = D == 64 ? 2 : 4;
+constexpr int PF_POLY = D == 64 ? 4 : 5;
 constexpr uint64_t PF_WAIT_NS = 4000000000ull;
 
 template <int D>
@@ -777,9 +779,8 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             const int tok = tok0 + r / group, head = it.kvh * group + r % group;
             const bool valid = tok < it.n;
             const int visible = valid ? max(w.first + tok + 1, 0) : 0;
-            // Keys that all of the warp's rows see, and that any does.
+            // Keys that all of the warp's rows see.
             const int clear = max(w.first + tok0 + (r - lane) / group + 1, 0);
-            const int seen = max(w.first + min(tok0 + (r - lane + 31) / group, it.n - 1) + 1, 0);
             float m = -INFINITY, l = 0.f;  // m: what the weights are relative to, unscaled
             for (int j = 0; j < mine; ++j) {
                 if (!wait(s_full(t), scores & 1)) break;
@@ -792,13 +793,16 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
 #pragma unroll
                 for (int c = 1; c < 4; ++c) tc_pin(x[c]);
                 const int key0 = (w.j0 + (w.halves ? 2 * j + t : j)) * PF_BN;
-                const bool masked = key0 + PF_BN > clear;
-                if (masked) {
+                if (key0 + PF_BN > clear) {
                     const int left = visible - key0;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
+                        {
+                        const int rest = left - c * 32;
+                        const uint32_t seen_bits = rest >= 32 ? ~0u : rest <= 0 ? 0u : (1u << rest) - 1u;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[c][i] = c * 32 + i < left ? x[c][i] : -INFINITY;
+                        for (int i = 0; i < 32; ++i) x[c][i] = (seen_bits >> i) & 1u ? x[c][i] : -INFINITY;
+                    }
                 }
                 float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -846,31 +850,14 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar);
                 };
-                if (!masked) {
-                    weigh(0);
-                    weigh(1);
-                    weigh(2);
-                    ready(p_most(t));
-                    weigh(3);
-                    ready(p_full(t));
-                } else {
-                    // Keys that none of the warp's rows sees weigh 0.
-                    const int some = seen - key0;
-                    auto weigh_some = [&](int c) {
-                        if (c * 32 < some) {
-                            weigh(c);
-                        } else {
-                            const uint32_t zero[16] = {};
-                            tc_st16(s_addr + c * 16, zero);
-                        }
-                    };
-                    weigh_some(0);
-                    weigh_some(1);
-                    weigh_some(2);
-                    ready(p_most(t));
-                    weigh_some(3);
-                    ready(p_full(t));
-                }
+                // One form for all tiles: a second one for masked tiles, which skips what none of the
+                // warp's rows sees, made the loop longer and every call 3 to 6% slower.
+                weigh(0);
+                weigh(1);
+                weigh(2);
+                ready(p_most(t));
+                weigh(3);
+                ready(p_full(t));
                 const float2 both = add2(sum[0], sum[1]);
                 l += both.x + both.y;
             }
