@@ -44,13 +44,12 @@ pa_status encode_pool(PFN_cuTensorMapEncodeTiled enc, CUtensorMap *map, CUtensor
 constexpr int kMaxDevices = 64;
 
 // Contexts are split where there are fewer items than kSplitItems an SM (a paged
-// call of few rows), into parts of kSplitTiles key tiles at least; a part costs
-// about kPartTiles key tiles beside its own (its start and end, its partial
-// result). Back to back, us at 3 / 6 items an SM: 512-token pieces of eight
-// 32768-token prompts 1969 (not split: 3.5 items an SM) / 1998 (two parts), 5-8
-// tokens over 4096-32768 110 / 113; at 24 the latter took 131.
-constexpr long long kSplitItems = 3;
-constexpr int kSplitTiles = 4, kPartTiles = 4;
+// call of few rows). The device deals their key tiles to the SMs in equal shares;
+// the workspace has room for kSplitMost times the parts that all contexts at their
+// longest would give. Not split, 512-token pieces of eight 32768-token prompts (3.5
+// items an SM) take 1969 us back to back, in two parts each 1998.
+constexpr long long kSplitItems = 3, kSplitMost = 4;
+constexpr int kSplitTiles = 4;  // key tiles of a part, at least
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -94,10 +93,11 @@ pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         done[dev].store(true, std::memory_order_release);
     }
-    // Every sequence has at most one tile that is not full.
+    // Every sequence has at most one tile that is not full. Dealt key tiles: a CTA an SM.
     const int tokens = pa::PF_NQ * pa::PF_BM / group;
-    const long long grid =
-        (p.num_tokens / tokens + (long long)std::min(p.num_seqs, p.num_tokens)) * p.num_kv_heads * max_parts;
+    const long long grid = max_parts > 1 ? sms
+                                         : (p.num_tokens / tokens + (long long)std::min(p.num_seqs, p.num_tokens)) *
+                                               p.num_kv_heads;
     if (grid >= (1ll << 31)) return fail(PA_ERR_UNSUPPORTED, "too many tiles");
     kernel<<<(unsigned)grid, SH::THREADS, SH::BYTES, stream>>>(p, maps);
     cudaError_t e = cudaGetLastError();
@@ -130,45 +130,28 @@ pa_status dispatch(pa::PrefillParams &p, int head_dim, int dtype, int max_parts,
                            : launch<64, __nv_bfloat16, PAGED>(p, max_parts, s);
 }
 
-// How contexts are split: key tiles of a part (0: they are not) and the parts
-// the longest one gives.
-struct Cut {
-    int split_tiles, max_parts;
-};
-
-Cut cut_of(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int max_keys, int sms) {
+// Parts that a context may be split into (1: it is not).
+int max_parts_of(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int max_keys, int sms) {
     const long long rows = (long long)num_tokens * (num_heads / num_kv_heads);
-    if ((long long)num_tokens * num_heads >= (1ll << 31)) return Cut{0, 1};
+    if ((long long)num_tokens * num_heads >= (1ll << 31)) return 1;
     const long long items =
         std::max<long long>(std::min(num_seqs, num_tokens), ceil_div(rows, pa::PF_NQ * pa::PF_BM)) * num_kv_heads;
     const int tiles = (int)ceil_div(max_keys, pa::PF_BN);
-    if (items >= kSplitItems * sms || tiles < 2 * kSplitTiles) return Cut{0, 1};
-    // Rounds of the SMs times the key tiles of a part, with what a part costs beside them.
-    const long long least = ceil_div(kSplitItems * sms, items);
-    long long best = 0, split = tiles;
-    for (long long parts = least; parts <= 4 * least && parts * kSplitTiles <= tiles; ++parts) {
-        const long long part = ceil_div(tiles, parts);
-        const long long cost = ceil_div(items * parts, sms) * (part + kPartTiles);
-        if (best == 0 || cost < best) {
-            best = cost;
-            split = part;
-        }
-    }
-    if (best == 0) split = kSplitTiles;  // too short for that: the shortest parts
-    const int max_parts = (int)ceil_div(tiles, split);
-    return max_parts > 1 ? Cut{(int)split, max_parts} : Cut{0, 1};
+    if (items >= kSplitItems * sms || tiles < 2 * kSplitTiles) return 1;
+    const long long least = std::max<long long>(kSplitTiles, ceil_div(items * tiles, kSplitMost * sms));
+    return (int)ceil_div(tiles - 1, least) + 2;
 }
 
 template <bool PAGED>
-pa_status run(pa::PrefillParams &p, const Cut &cut, int head_dim, float scale, int dtype, cudaStream_t s) {
+pa_status run(pa::PrefillParams &p, int max_parts, int head_dim, float scale, int dtype, cudaStream_t s) {
     // A negative scale is a positive one of the negated queries (the matrix
     // instruction negates them); 0 stands for the least positive one, so that
     // a masked score of -inf stays -inf.
     const float a = fabsf(scale) * 1.4426950408889634f;
     p.scale_log2 = a < FLT_MIN ? FLT_MIN : a;
     p.negate = scale < 0.f;
-    p.split_tiles = cut.split_tiles;
-    return dispatch<PAGED>(p, head_dim, dtype, cut.max_parts, s);
+    p.max_parts = max_parts;
+    return dispatch<PAGED>(p, head_dim, dtype, max_parts, s);
 }
 
 bool heads_supported(int num_heads, int num_kv_heads) {
@@ -225,7 +208,7 @@ pa_status pa_prefill(void *out, const void *q, const void *k, const void *v, con
     p.k_stride = k_stride;
     p.v_stride = v_stride;
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
-    return run<false>(p, Cut{0, 1}, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
+    return run<false>(p, 1, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
 }
 
 size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
@@ -237,9 +220,9 @@ size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_hea
     if (num_seqs == 0 || num_tokens == 0) return 256;
     int dev, sms;
     if (pa_internal_device(&dev, &sms) != PA_OK) return 0;
-    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, sms);
-    if (cut.max_parts == 1) return 256;
-    const size_t rows = (size_t)num_tokens * num_heads * cut.max_parts;
+    const int parts = max_parts_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, sms);
+    if (parts == 1) return 256;
+    const size_t rows = (size_t)num_tokens * num_heads * parts;
     return align256(rows * sizeof(float2)) + rows * head_dim * sizeof(float);
 }
 
@@ -291,11 +274,12 @@ pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const v
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
     int dev, sms;
     if ((st = pa_internal_device(&dev, &sms)) != PA_OK) return st;
-    const Cut cut = cut_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, sms);
-    const size_t rows = (size_t)num_tokens * num_heads * cut.max_parts;
+    const int parts = max_parts_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, sms);
+    p.sms = sms;
+    const size_t rows = (size_t)num_tokens * num_heads * parts;
     p.part_ml = static_cast<float2 *>(workspace);
     p.part_acc = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align256(rows * sizeof(float2)));
-    return run<true>(p, cut, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
+    return run<true>(p, parts, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -17,7 +17,7 @@ struct PrefillParams {
     long long q_stride, k_stride, v_stride;                     // elements from token to token
     float scale_log2;                                           // |scale| * log2(e), above 0
     bool negate;                                                // the scale is -scale_log2
-    int split_tiles;   // key tiles of a part of a context (paged), 0: contexts are not split
+    int sms, max_parts;  // parts that a context may be split into (paged), 1: it is not
     float *part_acc;   // [part][token][head][head_dim]: weighted values of the parts
     float2 *part_ml;   // [part][token][head]: what they are relative to (log2), sum of the weights
     unsigned int *errors;

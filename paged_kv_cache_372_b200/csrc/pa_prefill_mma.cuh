@@ -74,8 +74,8 @@ struct PrefillShape {
     static constexpr int S_COL = 0, O_COL = PF_NQ * 128;
     static constexpr int OFF_KV = PF_NQ * TILE;
     static constexpr int OFF_NEXT = OFF_KV + STAGES * TILE;  // 16 bytes: the launch taken over
-    static constexpr int OFF_ITEM = OFF_NEXT + 16;           // the work item, 8 integers
-    static constexpr int OFF_TMEM = OFF_ITEM + 32;           // TMEM address
+    static constexpr int OFF_ITEM = OFF_NEXT + 16;           // the work item, 10 integers
+    static constexpr int OFF_TMEM = OFF_ITEM + 48;           // TMEM address
     static constexpr int OFF_BAR = OFF_TMEM + 16;
     static constexpr int NUM_BARS = 2 * STAGES + 5 + 6 * PF_NQ;
     static constexpr int OFF_SWAP = OFF_BAR + (NUM_BARS + 1) / 2 * 16;  // the second tile's maxima and sums
@@ -276,9 +276,10 @@ __device__ __forceinline__ float2 ex2_fma(float2 x) {
 
 // ---- work items ---------------------------------------------------------------------------------------
 struct Item {
-    int s, tok0;            // sequence, first token of the tile among its rows
-    int row0, n, keys;      // as SeqRange
-    int part, parts, kvh;   // part of the context and their number, KV head
+    int s, tok0;           // sequence, first token of the tile among its rows
+    int row0, n, keys;     // as SeqRange
+    int part, parts, kvh;  // part of the context and their number, KV head
+    int j0, j1;            // key tiles of the part, where there are more than one
 };
 
 // Key tiles an item walks, [j0, j1), and how its two tiles of rows share them:
@@ -294,7 +295,7 @@ struct Walk {
 };
 
 // halves: whether items may be walked in halves (few rows over a paged context).
-__device__ __forceinline__ Walk walk_of(const Item &it, int tm, int split_tiles, bool halves) {
+__device__ __forceinline__ Walk walk_of(const Item &it, int tm, bool halves) {
     Walk w;
     w.first = it.keys - it.n;
     w.kv_end = 0;
@@ -307,8 +308,8 @@ __device__ __forceinline__ Walk walk_of(const Item &it, int tm, int split_tiles,
         w.kv_end = max(w.kv_end, w.end[t]);
     }
     const int all = (w.kv_end + PF_BN - 1) / PF_BN;
-    w.j0 = it.parts > 1 ? min(it.part * split_tiles, all) : 0;
-    w.j1 = it.parts > 1 ? min(w.j0 + split_tiles, all) : all;
+    w.j0 = it.parts > 1 ? min(it.j0, all) : 0;
+    w.j1 = it.parts > 1 ? min(it.j1, all) : all;
 #pragma unroll
     for (int t = 0; t < PF_NQ; ++t) w.count[t] = max(min(tiles[t], w.j1) - w.j0, 0);
     w.halves = halves && it.tok0 + tm >= it.n && w.count[0] > 1;
@@ -320,9 +321,33 @@ __device__ __forceinline__ Walk walk_of(const Item &it, int tm, int split_tiles,
     return w;
 }
 
-// Parts that the context of a sequence is split into.
-__device__ __forceinline__ int parts_of(int keys, int split_tiles) {
-    return split_tiles > 0 ? max((keys + split_tiles * PF_BN - 1) / (split_tiles * PF_BN), 1) : 1;
+// Few rows over long contexts: the key tiles of all (sequence, KV head, tile of
+// rows), a chain each and the chains one after the other, are dealt to the CTAs
+// in equal shares, cut where a share ends. A chain's parts are the shares it touches.
+struct Deal {
+    long long share;
+    int chains, tiles;  // of a sequence: chains of a KV head, key tiles of a chain
+
+    template <bool PAGED>
+    __device__ __forceinline__ static Deal of(const PrefillParams &p, const SeqRange &r, int TM) {
+        return Deal{0, (r.n + TM - 1) / TM, max((r.keys + PF_BN - 1) / PF_BN, 1)};
+    }
+    // Key tiles of a sequence's chains.
+    __device__ __forceinline__ long long all(const PrefillParams &p) const {
+        return (long long)chains * tiles * p.num_kv_heads;
+    }
+    // An equal share, but no chain in more parts than there is room for, nor in parts of less than 4.
+    __device__ __forceinline__ static long long share_of(const PrefillParams &p, long long sum, int longest) {
+        const long long even = (sum + p.sms - 1) / p.sms;
+        const int room = (longest - 1 + p.max_parts - 3) / (p.max_parts - 2);
+        return max(even, (long long)max(room, min(longest, 4)));
+    }
+};
+
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(FULL_MASK, x, o);
+    return x;
 }
 
 // Items are handed out from the longest to the shortest, roughly: a tile's
@@ -330,44 +355,100 @@ __device__ __forceinline__ int parts_of(int keys, int split_tiles) {
 // levels of their own and then 8 of them make one, and the items of a level
 // come sequence by sequence and head by head, so that the tiles that walk the
 // same keys run at the same time and share them in L2. (Heads first: a piece of
-// 512 tokens over 32768 read its keys from memory 3 times.) Where contexts are
-// split, parts are about equally long and there is one level. With C(d) the
+// 512 tokens over 32768 read its keys from memory 3 times.) With C(d) the
 // number of tiles of level d or above, item k has the level d with
 // C(d + 1) <= k / heads < C(d). One warp; its calls come with growing k.
 template <bool PAGED>
 struct Finder {
     int level = -1, above = 0, all = 0;  // C(level) = above <= the last k / heads; C(0) = all
-    int4 mine;                  // this lane's sequence among the first 32: base, count, parts
+    int2 mine;                  // this lane's sequence among the first 32: base, count
+    long long share = 0, at = 0, end = 0;  // this CTA's share of a deal
 
     __device__ __forceinline__ static int start(int d) { return d < 8 ? d : 8 * (d - 7); }
     __device__ __forceinline__ static int level_of(int position) { return position < 8 ? position : 7 + position / 8; }
 
-    __device__ __forceinline__ static void tiles(const PrefillParams &p, int s, int TM, int &base, int &count, int &parts,
+    __device__ __forceinline__ static void tiles(const PrefillParams &p, int s, int TM, int &base, int &count,
                                                  unsigned &bad) {
         const SeqRange r = seq_range<PAGED>(p, s, bad);
         count = (r.n + TM - 1) / TM;
-        parts = PAGED ? parts_of(r.keys, p.split_tiles) : 1;
-        base = PAGED && p.split_tiles == 0 ? max(r.keys - r.n, 0) / TM : 0;
+        base = max(r.keys - r.n, 0) / TM;
     }
 
+    __device__ __forceinline__ static void take(const PrefillParams &p, int s, Item &it, unsigned &bad) {
+        const SeqRange r = seq_range<PAGED>(p, s, bad);
+        it.s = s;
+        it.row0 = r.row0;
+        it.n = r.n;
+        it.keys = r.keys;
+    }
+
+    // The next piece of this CTA's share of a deal.
+    __device__ bool next_piece(const PrefillParams &p, int TM, Item &it, unsigned &bad) {
+        const int lane = threadIdx.x & 31, B = p.num_seqs;
+        if (share == 0) {
+            long long sum = 0;
+            int longest = 1;
+            for (int s = lane; s < B; s += 32) {
+                const Deal d = Deal::of<PAGED>(p, seq_range<PAGED>(p, s, bad), TM);
+                sum += d.all(p);
+                if (d.chains > 0) longest = max(longest, d.tiles);
+            }
+            sum = warp_sum(sum);
+            share = Deal::share_of(p, sum, __reduce_max_sync(FULL_MASK, longest));
+            at = min(share * blockIdx.x, sum);
+            end = min(at + share, sum);
+        }
+        if (at >= end) return false;
+        long long before = 0;
+        for (int s0 = 0; s0 < B; s0 += 32) {
+            Deal d{0, 0, 1};
+            if (s0 + lane < B) d = Deal::of<PAGED>(p, seq_range<PAGED>(p, s0 + lane, bad), TM);
+            long long sum = d.all(p);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(FULL_MASK, sum, o);
+                if (lane >= o) sum += up;
+            }
+            const unsigned m = __ballot_sync(FULL_MASK, before + sum > at);
+            if (m) {
+                const int src = __ffs(m) - 1;
+                const int chains = __shfl_sync(FULL_MASK, d.chains, src), tiles_of = __shfl_sync(FULL_MASK, d.tiles, src);
+                const long long in = at - before - __shfl_sync(FULL_MASK, sum - d.all(p), src);
+                const int chain = (int)(in / tiles_of);
+                it.j0 = (int)(in % tiles_of);
+                const long long start = at - it.j0;
+                it.part = (int)(blockIdx.x - start / share);
+                it.parts = (int)((start + tiles_of - 1) / share - start / share) + 1;
+                it.j1 = (int)min((long long)tiles_of, it.j0 + (end - at));
+                it.kvh = chain / chains;
+                it.tok0 = chain % chains * TM;
+                take(p, s0 + src, it, bad);
+                at += it.j1 - it.j0;
+                return true;
+            }
+            before += __shfl_sync(FULL_MASK, sum, 31);
+        }
+        return false;
+    }
+
+    // The kth item.
     __device__ bool find(const PrefillParams &p, int k, int TM, Item &it, unsigned &bad) {
         const int lane = threadIdx.x & 31, B = p.num_seqs, heads = p.num_kv_heads;
-        const bool split = PAGED && p.split_tiles > 0;
         auto count_above = [&](int d, int *top) {  // C(d), and the highest level + 1
             int c = 0, last = 0;
-            const int from = split ? 0 : start(d);
+            const int from = start(d);
             for (int s = lane; s < B; s += 32) {
-                int b = mine.x, n = mine.y, parts = mine.z;
-                if (s >= 32) tiles(p, s, TM, b, n, parts, bad);
-                c += max(0, min(n, b + n - from)) * parts;
-                if (n > 0) last = max(last, split ? 1 : level_of(b + n - 1) + 1);
+                int b = mine.x, n = mine.y;
+                if (s >= 32) tiles(p, s, TM, b, n, bad);
+                c += max(0, min(n, b + n - from));
+                if (n > 0) last = max(last, level_of(b + n - 1) + 1);
             }
             if (top) *top = __reduce_max_sync(FULL_MASK, last);
             return (int)__reduce_add_sync(FULL_MASK, c);
         };
         if (level < 0) {
-            mine = make_int4(0, 0, 1, 0);
-            if (lane < B) tiles(p, lane, TM, mine.x, mine.y, mine.z, bad);
+            mine = make_int2(0, 0);
+            if (lane < B) tiles(p, lane, TM, mine.x, mine.y, bad);
             all = count_above(0, &level);  // C(level) = 0
         }
         if (k >= all * heads) return false;
@@ -390,15 +471,15 @@ struct Finder {
         const int from = start(lo), to = start(lo + 1);
         for (int s0 = 0; s0 < B; s0 += 32) {
             const int s = s0 + lane;
-            int b = 0, n = 0, parts = 1, first = 0, last = 0;  // the sequence's tiles in this level
+            int b = 0, n = 0, first = 0, last = 0;  // the sequence's tiles in this level
             if (s < B) {
-                b = mine.x, n = mine.y, parts = mine.z;
-                if (s >= 32) tiles(p, s, TM, b, n, parts, bad);
-                first = split ? 0 : max(from - b, 0);
-                last = split ? n : min(n, to - b);
+                b = mine.x, n = mine.y;
+                if (s >= 32) tiles(p, s, TM, b, n, bad);
+                first = max(from - b, 0);
+                last = min(n, to - b);
             }
-            const int mine = max(last - first, 0) * parts * heads;
-            int sum = mine;
+            const int here = max(last - first, 0) * heads;
+            int sum = here;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int up = __shfl_up_sync(FULL_MASK, sum, o);
@@ -407,19 +488,14 @@ struct Finder {
             const unsigned m = __ballot_sync(FULL_MASK, sum > rank);
             if (m) {
                 const int src = __ffs(m) - 1;
-                const int at = rank - __shfl_sync(FULL_MASK, sum - mine, src);
+                const int in = rank - __shfl_sync(FULL_MASK, sum - here, src);
                 first = __shfl_sync(FULL_MASK, first, src);
                 last = __shfl_sync(FULL_MASK, last, src);
-                const int row = at / (last - first);  // part and head
-                it.s = s0 + src;
-                it.parts = __shfl_sync(FULL_MASK, parts, src);
-                it.kvh = row % heads;
-                it.part = row / heads;
-                it.tok0 = (last - 1 - at % (last - first)) * TM;
-                const SeqRange r = seq_range<PAGED>(p, it.s, bad);
-                it.row0 = r.row0;
-                it.n = r.n;
-                it.keys = r.keys;
+                it.kvh = in / (last - first);
+                it.tok0 = (last - 1 - in % (last - first)) * TM;
+                it.part = it.j0 = it.j1 = 0;
+                it.parts = 1;
+                take(p, s0 + src, it, bad);
                 return true;
             }
             rank -= __shfl_sync(FULL_MASK, sum, 31);
@@ -516,6 +592,8 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
         it.part = __shfl_sync(FULL_MASK, at[5], 0);
         it.parts = __shfl_sync(FULL_MASK, at[6], 0);
         it.kvh = __shfl_sync(FULL_MASK, at[7], 0);
+        it.j0 = __shfl_sync(FULL_MASK, at[8], 0);
+        it.j1 = __shfl_sync(FULL_MASK, at[9], 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(item_empty);
         return it.s >= 0;
@@ -530,7 +608,9 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             unsigned bad = 0;
             for (int nth = 0;; ++nth) {
                 Item it;
-                bool work = index >= 0 && finder.find(p, index, NQ * tm, it, bad);
+                const bool deal = PAGED && p.max_parts > 1;
+                const bool work = deal ? finder.next_piece(p, NQ * tm, it, bad)
+                                       : index >= 0 && finder.find(p, index, NQ * tm, it, bad);
                 if (!work) it.s = -1;
                 if (nth == 0 && __any_sync(FULL_MASK, bad != 0) && bad) atomicOr(p.errors, bad);
                 if (lane == 0) {
@@ -543,12 +623,15 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                     at[5] = it.part;
                     at[6] = it.parts;
                     at[7] = it.kvh;
+                    at[8] = it.j0;
+                    at[9] = it.j1;
                     mbar_arrive(item_full);
                 }
                 __syncwarp();
                 if (!work) break;
                 // When every warp has this item, the next launch is taken over.
                 if (!wait(item_empty, nth & 1)) break;
+                if (deal) continue;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(next_full, 16);
                     asm volatile(
@@ -576,7 +659,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             Item it;
             int c = 0, uses[NQ] = {};  // chunks (key or value tiles) issued; query tiles
             for (int nth = 0; alive && next_item(nth, it); ++nth) {
-                const Walk w = walk_of(it, tm, p.split_tiles, PAGED);
+                const Walk w = walk_of(it, tm, PAGED);
                 auto queries = [&](int t) {
                     if (w.count[t] == 0 || (uses[t] > 0 && !wait(q_empty(t), (uses[t] - 1) & 1))) return;
                     ++uses[t];
@@ -698,7 +781,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             Item it;
             int c = 0, uses = 0;  // chunks taken, query tiles
             for (int nth = 0; alive && next_item(nth, it); ++nth) {
-                const Walk w = walk_of(it, tm, p.split_tiles, PAGED);
+                const Walk w = walk_of(it, tm, PAGED);
                 const int tiles = w.j1 - w.j0, mine = t == 0 ? w.count[0] : w.count[1];
                 if (tiles == 0) continue;
                 // Keys of tile j that any row of this one sees, in the steps of 16 of the products.
@@ -773,7 +856,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
         Item it;
         int scores = 0, results0 = 0, results1 = 0, pairs = 0;  // tiles of scores taken, accumulators, items in halves
         for (int nth = 0; alive && next_item(nth, it); ++nth) {
-            const Walk w = walk_of(it, tm, p.split_tiles, PAGED);
+            const Walk w = walk_of(it, tm, PAGED);
             const int mine = t == 0 ? w.count[0] : w.count[1];
             const int r = quarter * 32 + lane, tok0 = it.tok0 + (w.halves ? 0 : t * tm);  // row of the tile
             const int tok = tok0 + r / group, head = it.kvh * group + r % group;
@@ -998,9 +1081,33 @@ __global__ void __launch_bounds__(128) pa_prefill_join_kernel(const __grid_const
         else
             hi = mid;
     }
+    // The parts of its chain, from all sequences' chains.
+    __shared__ long long sums[4][2];
+    __shared__ int most[4];
     unsigned bad = 0;
+    const int group = p.num_heads / p.num_kv_heads, TM = PF_NQ * PF_BM / group;
+    long long sum = 0, before = 0;
+    int longest = 1;
+    for (int s = threadIdx.x; s < p.num_seqs; s += 128) {
+        const Deal d = Deal::of<true>(p, seq_range<true>(p, s, bad), TM);
+        sum += d.all(p);
+        before += s < lo ? d.all(p) : 0;
+        if (d.chains > 0) longest = max(longest, d.tiles);
+    }
+    sum = warp_sum(sum);
+    before = warp_sum(before);
+    longest = __reduce_max_sync(FULL_MASK, longest);
+    if (lane == 0) sums[warp][0] = sum, sums[warp][1] = before, most[warp] = longest;
+    __syncthreads();
+    sum = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
+    before = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
+    longest = max(max(most[0], most[1]), max(most[2], most[3]));
     const SeqRange r = seq_range<true>(p, lo, bad);
-    const int parts = parts_of(r.keys, p.split_tiles);
+    const Deal d = Deal::of<true>(p, r, TM);
+    const long long share = Deal::share_of(p, sum, longest);
+    const int chain = (item % p.num_heads) / group * d.chains + (row - r.row0) / TM;
+    const long long start = before + (long long)chain * d.tiles;
+    const int parts = (int)((start + d.tiles - 1) / share - start / share) + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention launch before this one is done
     if (row < r.row0 || row >= r.row0 + r.n || parts == 1) return;
     const size_t stride = (size_t)p.num_tokens * p.num_heads;
