@@ -218,3 +218,33 @@ def test_prefill_far_from_the_diagonal_is_split_over_the_running_maximum():
         k[:, 0, 0] = (torch.arange(n, device="cuda") // 128) * step * math.log(2.0)
         v = normal((n, 1, D), torch.bfloat16, gen(50))
         run_packed(q, k, v, [0, n], 1.0)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_dealt_key_tiles(seed):
+    """Few rows over contexts of any lengths, more than 32 sequences among them, limits far above the contexts."""
+    g = torch.Generator().manual_seed(100 + seed)
+
+    def pick(*x):
+        return x[int(torch.randint(0, len(x), (1,), generator=g))]
+
+    B = pick(1, 2, 5, 33, 70)
+    Hkv = pick(1, 2)
+    H = Hkv * pick(1, 2, 4, 8)
+    D, bs, dtype = pick(64, 128), pick(16, 32, 64), pick(torch.float16, torch.bfloat16)
+    top = pick(3, 200, 1500) if B > 5 else pick(40, 3000, 9000)
+    ctx = torch.randint(0, top + 1, (B,), generator=g).tolist()
+    new = [int(torch.randint(0, 12, (1,), generator=g)) if torch.rand(1, generator=g) < 0.8 else 0 for _ in ctx]
+    if sum(new) == 0:
+        new[0] = 1
+    if max(ctx) == 0:
+        ctx[0] = top
+    limit = pick(max(ctx), 9216, 65536)
+    q, kp, vp, table, cu = pooled(ctx, new, H, Hkv, D, bs, dtype, seed, stale=float("nan") if seed % 2 else None)
+    wide = torch.full((B, -(-max(limit, 1) // bs)), -1, dtype=I32, device="cuda")
+    wide[:, :min(table.shape[1], wide.shape[1])] = table[:, :wide.shape[1]]
+    first = run_paged(q, kp, vp, wide, ctx, cu, 0.08, limit)
+    ws = pa.alloc_prefill_workspace(B, q.shape[0], H, Hkv, D, bs, limit)
+    ws.fill_(255)
+    again = run_paged(q, kp, vp, wide, ctx, cu, 0.08, limit, ws)
+    assert torch.equal(bits(first), bits(again))
