@@ -24,13 +24,14 @@
 // product run ahead of the item's end; with a CTA for each item its set-up and end
 // cost 16,000 clocks, as much as five key tiles. Items come longest first.
 //
-// Measured (head size 128): a key tile of both tiles of rows takes about 2,750
+// Measured (head size 128): a key tile of both tiles of rows takes about 2,700
 // clocks, 2,048 of them products: the chain of a tile of rows (scores 512, to
-// registers 150, maximum 300, exponentials 1,250, hand-over twice 200, last
+// registers 150, maximum 300, exponentials 1,200, hand-over twice 200, last
 // quarter of the product 128) is what remains, and two chains are all that the
-// 512 columns of TMEM hold. 16384 tokens, 32/8 heads, bf16: 1.55 ms after a pause
-// (1,420 TFLOP/s at 1.8 GHz), 1.80 ms back to back, where 1,000 W hold the clock
-// at 1.45 GHz. The tensor pipe is active 70% of the time.
+// 512 columns of TMEM hold. 16384 tokens, 32/8 heads, bf16: 1.50 ms after a pause
+// (1,467 TFLOP/s at 1.8 GHz), 1.77 ms back to back, where 1,000 W hold the clock
+// at 1.45 GHz. The tensor pipe is active 75% of the time. 5-8 tokens of 8 requests
+// over 4096-32768 tokens: 91 us, 5.3 TB/s of the cache.
 //
 // Masked places: S is replaced by -inf there (a selection, so NaN and
 // infinities in masked keys do not spread) and P is 0. A NaN or infinity in a
