@@ -16,6 +16,7 @@ import os
 import re
 import shutil
 import subprocess
+import time
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -81,6 +82,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     if not force and out is None and not stale():
         return LIB
     os.makedirs(os.path.dirname(target), exist_ok=True)
+    started = time.time()
     common = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE]
     if verbose:
@@ -99,12 +101,15 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
 
     def compile_one(job: tuple[str, str]) -> None:
         src, obj = job
+        begun = time.time()
         _run([*common, "-c", src, "-o", obj + suffix], verbose)
+        os.utime(obj + suffix, (begun, begun))  # a source edited meanwhile is newer
         os.replace(obj + suffix, obj)
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 1))) as pool:
         list(pool.map(compile_one, todo))
     _run([nvcc(), *ARCH, "-shared", *objects, "-o", target + suffix], False)
+    os.utime(target + suffix, (started, started))
     os.replace(target + suffix, target)
     return target
 
