@@ -1,48 +1,10 @@
 // Device side of the prompt attention (pa_prefill, pa_prefill_paged;
-// include/pa.h): parameters, the rows of a sequence and the row-at-a-time form.
+// include/pa.h): the row-at-a-time form.
 #pragma once
 
-#include "pa_common.cuh"
+#include "pa_prefill_plan.cuh"
 
 namespace pa {
-
-struct PrefillParams {
-    void *out;
-    const void *q;
-    const void *k, *v;  // packed rows, or the pools
-    const int32_t *cu_seqlens;
-    const int32_t *block_tables, *context_lens;  // paged only
-    int num_seqs, num_tokens, num_heads, num_kv_heads;
-    int block_size, max_blocks_per_seq, num_blocks, ctx_limit;  // paged only
-    long long q_stride, k_stride, v_stride;                     // elements from token to token
-    float scale_log2;                                           // |scale| * log2(e), above 0
-    bool negate;                                                // the scale is -scale_log2
-    int sms, max_parts;  // parts that a context may be split into (paged), 1: it is not
-    float *part_acc;   // [part][token][head][head_dim]: weighted values of the parts
-    float2 *part_ml;   // [part][token][head]: what they are relative to (log2), sum of the weights
-    unsigned int *errors;
-};
-
-// Query rows [row0, row0 + n) of sequence s and the keys it has; row i of them
-// sees the first keys - n + i + 1.
-struct SeqRange {
-    int row0, n, keys;
-};
-
-template <bool PAGED>
-__device__ __forceinline__ SeqRange seq_range(const PrefillParams &p, int s, unsigned &bad) {
-    int a = p.cu_seqlens[s], b = p.cu_seqlens[s + 1];
-    if (a < 0 || b < a || b > p.num_tokens) bad |= PA_DEVERR_TOKENS;
-    a = min(max(a, 0), p.num_tokens);
-    b = min(max(b, a), p.num_tokens);
-    SeqRange r{a, b - a, b - a};
-    if constexpr (PAGED) {
-        const int c = p.context_lens[s];
-        if (c < 0 || c > p.ctx_limit) bad |= PA_DEVERR_CONTEXT;
-        r.keys = min(max(c, 0), p.ctx_limit);
-    }
-    return r;
-}
 
 // What a row has from a range of keys: weighted values relative to the maximum
 // m (log2 units) and the sum of the weights; D / 32 elements a lane.

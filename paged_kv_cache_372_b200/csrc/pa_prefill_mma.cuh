@@ -48,9 +48,6 @@
 
 namespace pa {
 
-constexpr int PF_NQ = 2;    // tiles of rows of an item
-constexpr int PF_BM = 128;  // rows of a tile
-constexpr int PF_BN = 128;  // keys of a tile
 // Of 16 pairs of exponentials, those on the FMA units. 8192 tokens, 32/8 heads of
 // 64, us at 0 / 2 / 4 / 6 / 8 pairs: bf16 350 / 385 / 340 / 345 / 367, fp16 352 / 374 /
 // 340 / 345 / 381; 16384 tokens, heads of 128, bf16, at 3 / 4 / 5 / 6: 1585 / 1510 / 1495 / 1493,
@@ -274,236 +271,6 @@ __device__ __forceinline__ float2 ex2_fma(float2 x) {
     y.y = __int_as_float(__float_as_int(y.y) + (__float_as_int(r.y) << 23));
     return y;
 }
-
-// ---- work items ---------------------------------------------------------------------------------------
-struct Item {
-    int s, tok0;           // sequence, first token of the tile among its rows
-    int row0, n, keys;     // as SeqRange
-    int part, parts, kvh;  // part of the context and their number, KV head
-    int j0, j1;            // key tiles of the part, where there are more than one
-};
-
-// Key tiles an item walks, [j0, j1), and how its two tiles of rows share them:
-// each walks all that its rows see. Where the second has no rows (the last rows of
-// a prompt, few rows over a long context) both take the first one's rows, one the
-// even and one the odd key tiles, and their results are joined at the end: one
-// tile of rows alone would wait for its softmax half of the time.
-struct Walk {
-    int first;           // row i of the sequence sees the keys below first + i + 1
-    int j0, j1, kv_end;  // kv_end: the keys that any of the rows sees
-    bool halves;
-    int count[PF_NQ], end[PF_NQ];  // key tiles of a tile of rows, the keys that any of its rows sees
-};
-
-// halves: whether items may be walked in halves (few rows over a paged context).
-__device__ __forceinline__ Walk walk_of(const Item &it, int tm, bool halves) {
-    Walk w;
-    w.first = it.keys - it.n;
-    w.kv_end = 0;
-    int tiles[PF_NQ];
-#pragma unroll
-    for (int t = 0; t < PF_NQ; ++t) {
-        const int a = it.tok0 + t * tm, b = min(it.n, a + tm);
-        w.end[t] = a < b ? max(w.first + b, 0) : 0;
-        tiles[t] = (w.end[t] + PF_BN - 1) / PF_BN;
-        w.kv_end = max(w.kv_end, w.end[t]);
-    }
-    const int all = (w.kv_end + PF_BN - 1) / PF_BN;
-    w.j0 = it.parts > 1 ? min(it.j0, all) : 0;
-    w.j1 = it.parts > 1 ? min(it.j1, all) : all;
-#pragma unroll
-    for (int t = 0; t < PF_NQ; ++t) w.count[t] = max(min(tiles[t], w.j1) - w.j0, 0);
-    w.halves = halves && it.tok0 + tm >= it.n && w.count[0] > 1;
-    if (w.halves) {
-        w.count[1] = w.count[0] / 2;
-        w.count[0] -= w.count[1];
-        w.end[1] = w.end[0];
-    }
-    return w;
-}
-
-// Few rows over long contexts: the key tiles of all (sequence, KV head, tile of
-// rows), a chain each and the chains one after the other, are dealt to the CTAs
-// in equal shares, cut where a share ends. A chain's parts are the shares it touches.
-struct Deal {
-    long long share;
-    int chains, tiles;  // of a sequence: chains of a KV head, key tiles of a chain
-
-    template <bool PAGED>
-    __device__ __forceinline__ static Deal of(const PrefillParams &p, const SeqRange &r, int TM) {
-        return Deal{0, (r.n + TM - 1) / TM, max((r.keys + PF_BN - 1) / PF_BN, 1)};
-    }
-    // Key tiles of a sequence's chains.
-    __device__ __forceinline__ long long all(const PrefillParams &p) const {
-        return (long long)chains * tiles * p.num_kv_heads;
-    }
-    // An equal share, but no chain in more parts than there is room for, nor in parts of less than 4.
-    __device__ __forceinline__ static long long share_of(const PrefillParams &p, long long sum, int longest) {
-        const long long even = (sum + p.sms - 1) / p.sms;
-        const int room = (longest - 1 + p.max_parts - 3) / (p.max_parts - 2);
-        return max(even, (long long)max(room, min(longest, 4)));
-    }
-};
-
-__device__ __forceinline__ long long warp_sum(long long x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(FULL_MASK, x, o);
-    return x;
-}
-
-// Items are handed out from the longest to the shortest, roughly: a tile's
-// position in its context counts in units of TM tokens, positions 0 to 7 are
-// levels of their own and then 8 of them make one, and the items of a level
-// come sequence by sequence and head by head, so that the tiles that walk the
-// same keys run at the same time and share them in L2. (Heads first: a piece of
-// 512 tokens over 32768 read its keys from memory 3 times.) With C(d) the
-// number of tiles of level d or above, item k has the level d with
-// C(d + 1) <= k / heads < C(d). One warp; its calls come with growing k.
-template <bool PAGED>
-struct Finder {
-    int level = -1, above = 0, all = 0;  // C(level) = above <= the last k / heads; C(0) = all
-    int2 mine;                  // this lane's sequence among the first 32: base, count
-    long long share = 0, at = 0, end = 0;  // this CTA's share of a deal
-
-    __device__ __forceinline__ static int start(int d) { return d < 8 ? d : 8 * (d - 7); }
-    __device__ __forceinline__ static int level_of(int position) { return position < 8 ? position : 7 + position / 8; }
-
-    __device__ __forceinline__ static void tiles(const PrefillParams &p, int s, int TM, int &base, int &count,
-                                                 unsigned &bad) {
-        const SeqRange r = seq_range<PAGED>(p, s, bad);
-        count = (r.n + TM - 1) / TM;
-        base = max(r.keys - r.n, 0) / TM;
-    }
-
-    __device__ __forceinline__ static void take(const PrefillParams &p, int s, Item &it, unsigned &bad) {
-        const SeqRange r = seq_range<PAGED>(p, s, bad);
-        it.s = s;
-        it.row0 = r.row0;
-        it.n = r.n;
-        it.keys = r.keys;
-    }
-
-    // The next piece of this CTA's share of a deal.
-    __device__ bool next_piece(const PrefillParams &p, int TM, Item &it, unsigned &bad) {
-        const int lane = threadIdx.x & 31, B = p.num_seqs;
-        if (share == 0) {
-            long long sum = 0;
-            int longest = 1;
-            for (int s = lane; s < B; s += 32) {
-                const Deal d = Deal::of<PAGED>(p, seq_range<PAGED>(p, s, bad), TM);
-                sum += d.all(p);
-                if (d.chains > 0) longest = max(longest, d.tiles);
-            }
-            sum = warp_sum(sum);
-            share = Deal::share_of(p, sum, __reduce_max_sync(FULL_MASK, longest));
-            at = min(share * blockIdx.x, sum);
-            end = min(at + share, sum);
-        }
-        if (at >= end) return false;
-        long long before = 0;
-        for (int s0 = 0; s0 < B; s0 += 32) {
-            Deal d{0, 0, 1};
-            if (s0 + lane < B) d = Deal::of<PAGED>(p, seq_range<PAGED>(p, s0 + lane, bad), TM);
-            long long sum = d.all(p);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long up = __shfl_up_sync(FULL_MASK, sum, o);
-                if (lane >= o) sum += up;
-            }
-            const unsigned m = __ballot_sync(FULL_MASK, before + sum > at);
-            if (m) {
-                const int src = __ffs(m) - 1;
-                const int chains = __shfl_sync(FULL_MASK, d.chains, src), tiles_of = __shfl_sync(FULL_MASK, d.tiles, src);
-                const long long in = at - before - __shfl_sync(FULL_MASK, sum - d.all(p), src);
-                const int chain = (int)(in / tiles_of);
-                it.j0 = (int)(in % tiles_of);
-                const long long start = at - it.j0;
-                it.part = (int)(blockIdx.x - start / share);
-                it.parts = (int)((start + tiles_of - 1) / share - start / share) + 1;
-                it.j1 = (int)min((long long)tiles_of, it.j0 + (end - at));
-                it.kvh = chain / chains;
-                it.tok0 = chain % chains * TM;
-                take(p, s0 + src, it, bad);
-                at += it.j1 - it.j0;
-                return true;
-            }
-            before += __shfl_sync(FULL_MASK, sum, 31);
-        }
-        return false;
-    }
-
-    // The kth item.
-    __device__ bool find(const PrefillParams &p, int k, int TM, Item &it, unsigned &bad) {
-        const int lane = threadIdx.x & 31, B = p.num_seqs, heads = p.num_kv_heads;
-        auto count_above = [&](int d, int *top) {  // C(d), and the highest level + 1
-            int c = 0, last = 0;
-            const int from = start(d);
-            for (int s = lane; s < B; s += 32) {
-                int b = mine.x, n = mine.y;
-                if (s >= 32) tiles(p, s, TM, b, n, bad);
-                c += max(0, min(n, b + n - from));
-                if (n > 0) last = max(last, level_of(b + n - 1) + 1);
-            }
-            if (top) *top = __reduce_max_sync(FULL_MASK, last);
-            return (int)__reduce_add_sync(FULL_MASK, c);
-        };
-        if (level < 0) {
-            mine = make_int2(0, 0);
-            if (lane < B) tiles(p, lane, TM, mine.x, mine.y, bad);
-            all = count_above(0, &level);  // C(level) = 0
-        }
-        if (k >= all * heads) return false;
-        int lo = 0, hi = level, before = above;  // C(lo) > k / heads >= C(hi) = before
-        for (int step = 1; hi - lo > 1;) {
-            const int mid = step < 4 ? max(hi - step, 1) : (lo + hi) >> 1;  // most often one of the next levels
-            step *= 2;
-            const int c = count_above(mid, nullptr);
-            if (c * heads > k) {
-                lo = mid;
-                step = 4;
-            } else {
-                hi = mid;
-                before = c;
-            }
-        }
-        level = hi;
-        above = before;
-        int rank = k - before * heads;  // within level lo
-        const int from = start(lo), to = start(lo + 1);
-        for (int s0 = 0; s0 < B; s0 += 32) {
-            const int s = s0 + lane;
-            int b = 0, n = 0, first = 0, last = 0;  // the sequence's tiles in this level
-            if (s < B) {
-                b = mine.x, n = mine.y;
-                if (s >= 32) tiles(p, s, TM, b, n, bad);
-                first = max(from - b, 0);
-                last = min(n, to - b);
-            }
-            const int here = max(last - first, 0) * heads;
-            int sum = here;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(FULL_MASK, sum, o);
-                if (lane >= o) sum += up;
-            }
-            const unsigned m = __ballot_sync(FULL_MASK, sum > rank);
-            if (m) {
-                const int src = __ffs(m) - 1;
-                const int in = rank - __shfl_sync(FULL_MASK, sum - here, src);
-                first = __shfl_sync(FULL_MASK, first, src);
-                last = __shfl_sync(FULL_MASK, last, src);
-                it.kvh = in / (last - first);
-                it.tok0 = (last - 1 - in % (last - first)) * TM;
-                it.part = it.j0 = it.j1 = 0;
-                it.parts = 1;
-                take(p, s0 + src, it, bad);
-                return true;
-            }
-            rank -= __shfl_sync(FULL_MASK, sum, 31);
-        }
-        return false;
-    }
-};
 
 struct PrefillMaps {
     CUtensorMap q, k, v;
