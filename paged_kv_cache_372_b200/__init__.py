@@ -142,6 +142,22 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _scratch(alloc, stream, dev, *args, **kw) -> torch.Tensor:
+    """alloc(*args, **kw) with the stream that will use the memory current.
+
+    The allocator hands out a freed block at once to the stream it belongs to,
+    whose work is ordered behind the block's last use, and gets it back as soon
+    as this call's tensor is dropped. A block of another stream's pool may still
+    be written by work there.
+    """
+    if stream is None:
+        return alloc(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return alloc(*args, **kw)
+
+
 def _cuda(t: torch.Tensor, name: str, dtype=None) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -756,10 +772,7 @@ def pa_prefill_paged(out, q, k_pool, v_pool, block_tables, context_lens, cu_seql
     pool = (NB, Hkv, bs, D)
     B, W = tables = block_tables.shape
     if workspace is None:
-        workspace = alloc_prefill_workspace(B, T, H, Hkv, D, bs, max_context_len, dev)
-        if stream is not None:
-            # Allocated on the current stream, used on another: kept until that one has passed.
-            workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), device=dev))
+        workspace = _scratch(alloc_prefill_workspace, stream, dev, B, T, H, Hkv, D, bs, max_context_len, dev)
     elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     _call(lib().pa_prefill_paged, dev, stream, _full(out, "out", shape, dt, dev), q.data_ptr(),
