@@ -241,7 +241,8 @@ def pa_decode(out, q, k_pool, v_pool, block_tables, context_lens, scale, max_con
     if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
         raise ValueError("block_tables must be [B][W] and context_lens [B]")
     if workspace is None:
-        workspace = alloc_workspace(B, H, Hkv, D, bs, max_context_len, partition_size, q.device)
+        workspace = _scratch(alloc_workspace, stream, q.device, B, H, Hkv, D, bs, max_context_len, partition_size,
+                             q.device)
     _check(lib().pa_decode(
         _cuda(out, "out"), _cuda(q, "q"), _cuda(k_pool, "k_pool"), _cuda(v_pool, "v_pool"),
         _cuda(block_tables, "block_tables", torch.int32), _cuda(context_lens, "context_lens", torch.int32),
@@ -261,7 +262,8 @@ def pa_decode_append(out, q, k_new, v_new, k_pool, v_pool, block_tables, context
     if k_new.dtype != q.dtype or v_new.dtype != q.dtype or k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
         raise ValueError("q, k_new, v_new and the pools must share one dtype")
     if workspace is None:
-        workspace = alloc_workspace(B, H, Hkv, D, bs, max_context_len, partition_size, q.device)
+        workspace = _scratch(alloc_workspace, stream, q.device, B, H, Hkv, D, bs, max_context_len, partition_size,
+                             q.device)
     _check(lib().pa_decode_append(
         _cuda(out, "out"), _cuda(q, "q"), _cuda(k_new, "k_new"), _cuda(v_new, "v_new"), _cuda(k_pool, "k_pool"),
         _cuda(v_pool, "v_pool"), _cuda(block_tables, "block_tables", torch.int32),
@@ -291,7 +293,8 @@ def pa_decode_shared(out, q, k_pool, v_pool, block_tables, context_lens, scale, 
     if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
         raise ValueError("block_tables must be [B][W] and context_lens [B]")
     if workspace is None:
-        workspace = alloc_workspace(B, H, Hkv, D, bs, max_context_len, partition_size, q.device, shared=True)
+        workspace = _scratch(alloc_workspace, stream, q.device, B, H, Hkv, D, bs, max_context_len, partition_size,
+                             q.device, shared=True)
     _check(lib().pa_decode_shared(
         _cuda(out, "out"), _cuda(q, "q"), None if k_new is None else _cuda(k_new, "k_new"),
         None if v_new is None else _cuda(v_new, "v_new"), _cuda(k_pool, "k_pool"), _cuda(v_pool, "v_pool"),
@@ -315,7 +318,8 @@ def pa_decode_fp8(out, q, k_pool, v_pool, block_tables, context_lens, scale, max
     if q.dtype not in _DTYPES or out.dtype != q.dtype:
         raise ValueError("q and out must share one dtype, fp16 or bf16")
     if workspace is None:
-        workspace = alloc_workspace(B, H, Hkv, D, bs, max_context_len, partition_size, q.device, fp8=True)
+        workspace = _scratch(alloc_workspace, stream, q.device, B, H, Hkv, D, bs, max_context_len, partition_size,
+                             q.device, fp8=True)
     _check(lib().pa_decode_fp8(
         _cuda(out, "out"), _cuda(q, "q"), _cuda(k_pool, "k_pool"), _cuda(v_pool, "v_pool"),
         _cuda(block_tables, "block_tables", torch.int32), _cuda(context_lens, "context_lens", torch.int32),
@@ -380,7 +384,8 @@ def pa_decode_quant(out, q, k_pool, v_pool, block_tables, context_lens, scale, m
     if q.dtype not in _DTYPES or out.dtype != q.dtype:
         raise ValueError("q and out must share one dtype, fp16 or bf16")
     if workspace is None:
-        workspace = alloc_workspace(B, H, Hkv, D, bs, max_context_len, partition_size, q.device, fp8=True)
+        workspace = _scratch(alloc_workspace, stream, q.device, B, H, Hkv, D, bs, max_context_len, partition_size,
+                             q.device, fp8=True)
     _check(lib().pa_decode_quant(
         _cuda(out, "out"), _cuda(q, "q"), _cuda(k_pool, "k_pool"), _cuda(v_pool, "v_pool"),
         _cuda(block_tables, "block_tables", torch.int32), _cuda(context_lens, "context_lens", torch.int32),
@@ -421,7 +426,8 @@ def pa_decode_quant_blocks(out, q, k_pool, v_pool, block_tables, context_lens, s
     if q.dtype not in _DTYPES or out.dtype != q.dtype:
         raise ValueError("q and out must share one dtype, fp16 or bf16")
     if workspace is None:
-        workspace = alloc_workspace(B, H, Hkv, D, bs, max_context_len, partition_size, q.device, fp8=True)
+        workspace = _scratch(alloc_workspace, stream, q.device, B, H, Hkv, D, bs, max_context_len, partition_size,
+                             q.device, fp8=True)
     _check(lib().pa_decode_quant_blocks(
         _cuda(out, "out"), _cuda(q, "q"), _cuda(k_pool, "k_pool"), _cuda(v_pool, "v_pool"),
         _cuda(block_tables, "block_tables", torch.int32), _cuda(context_lens, "context_lens", torch.int32),
@@ -445,7 +451,8 @@ def pa_decode_shared_quant(out, q, k_pool, v_pool, block_tables, context_lens, s
     if q.dtype not in _DTYPES or out.dtype != q.dtype:
         raise ValueError("q and out must share one dtype, fp16 or bf16")
     if workspace is None:
-        workspace = alloc_workspace(B, H, Hkv, D, bs, max_context_len, partition_size, q.device, shared=True)
+        workspace = _scratch(alloc_workspace, stream, q.device, B, H, Hkv, D, bs, max_context_len, partition_size,
+                             q.device, shared=True)
     _check(lib().pa_decode_shared_quant(
         _cuda(out, "out"), _cuda(q, "q"), _cuda(k_pool, "k_pool"), _cuda(v_pool, "v_pool"),
         _cuda(block_tables, "block_tables", torch.int32), _cuda(context_lens, "context_lens", torch.int32),
@@ -470,7 +477,8 @@ def pa_decode_shared_quant_blocks(out, q, k_pool, v_pool, block_tables, context_
     if q.dtype not in _DTYPES or out.dtype != q.dtype:
         raise ValueError("q and out must share one dtype, fp16 or bf16")
     if workspace is None:
-        workspace = alloc_workspace(B, H, Hkv, D, bs, max_context_len, partition_size, q.device, shared=True)
+        workspace = _scratch(alloc_workspace, stream, q.device, B, H, Hkv, D, bs, max_context_len, partition_size,
+                             q.device, shared=True)
     _check(lib().pa_decode_shared_quant_blocks(
         _cuda(out, "out"), _cuda(q, "q"), _cuda(k_pool, "k_pool"), _cuda(v_pool, "v_pool"),
         _cuda(block_tables, "block_tables", torch.int32), _cuda(context_lens, "context_lens", torch.int32),

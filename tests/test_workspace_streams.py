@@ -63,3 +63,33 @@ def test_prefill_paged_allocates_on_its_stream(streams, monkeypatch, stream, han
     with pytest.raises(Allocated) as e:
         pa.pa_prefill_paged(q, q, pool, pool, tab, ctx, cu, 0.1, 64, stream=stream)
     assert e.value.args[0] == handle
+
+
+S, P8 = "e4m3", torch.uint8
+DECODES = {
+    "pa_decode": lambda q, kv, kp, k8, c, **kw: pa.pa_decode(q, q, kp, kp, *c, **kw),
+    "pa_decode_append": lambda q, kv, kp, k8, c, **kw: pa.pa_decode_append(q, q, kv, kv, kp, kp, *c, **kw),
+    "pa_decode_shared": lambda q, kv, kp, k8, c, **kw: pa.pa_decode_shared(q, q, kp, kp, *c, **kw),
+    "pa_decode_fp8": lambda q, kv, kp, k8, c, **kw: pa.pa_decode_fp8(q, q, k8, k8, *c, 1.0, 1.0, **kw),
+    "pa_decode_quant": lambda q, kv, kp, k8, c, **kw: pa.pa_decode_quant(q, q, k8, k8, *c, S, None, None, **kw),
+    "pa_decode_quant_blocks":
+        lambda q, kv, kp, k8, c, **kw: pa.pa_decode_quant_blocks(q, q, k8, k8, *c, S, None, None, **kw),
+    "pa_decode_shared_quant":
+        lambda q, kv, kp, k8, c, **kw: pa.pa_decode_shared_quant(q, q, k8, k8, *c, S, None, None, **kw),
+    "pa_decode_shared_quant_blocks":
+        lambda q, kv, kp, k8, c, **kw: pa.pa_decode_shared_quant_blocks(q, q, k8, k8, *c, S, None, None, **kw),
+}
+
+
+@pytest.mark.parametrize("name", DECODES)
+@pytest.mark.parametrize("stream,handle", [(None, 0), (FakeStream(77), 77), (88, 88)])
+def test_decode_allocates_on_its_stream(streams, monkeypatch, name, stream, handle):
+    def alloc(*a, **kw):
+        raise Allocated(streams[-1])
+
+    monkeypatch.setattr(pa, "alloc_workspace", alloc)
+    q, kv, kp, k8 = fake(2, 2, 64), fake(2, 2, 64), fake(3, 2, 16, 64), fake(3, 2, 16, 64, dtype=P8)
+    tab, ctx = fake(2, 4, dtype=torch.int32), fake(2, dtype=torch.int32)
+    with pytest.raises(Allocated) as e:
+        DECODES[name](q, kv, kp, k8, (tab, ctx, 0.1, 64), stream=stream)
+    assert e.value.args[0] == handle
