@@ -746,7 +746,8 @@ def pa_prefill(out, q, k, v, cu_seqlens, scale, stream=None) -> torch.Tensor:
 
 def pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
                                     max_context_len) -> int:
-    """Workspace bytes of pa_prefill_paged on the current device."""
+    """Workspace bytes for pa_prefill_paged on the current device: enough for calls with at most these num_seqs,
+    num_tokens and max_context_len."""
     n = int(lib().pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
                                                   max_context_len))
     if n == 0:
@@ -756,7 +757,7 @@ def pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_head
 
 def alloc_prefill_workspace(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
                             device=None) -> torch.Tensor:
-    """Workspace for pa_prefill_paged."""
+    """Workspace for pa_prefill_paged calls with at most these num_seqs, num_tokens and max_context_len."""
     with torch.cuda.device(device):
         n = pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
                                             max_context_len)

@@ -44,17 +44,26 @@ pa_status encode_pool(PFN_cuTensorMapEncodeTiled enc, CUtensorMap *map, CUtensor
 constexpr int kMaxDevices = 64;
 
 // Contexts are split where there are fewer items than kSplitItems an SM (a paged
-// call of few rows). The device deals their key tiles to the SMs in equal shares;
-// the workspace has room for kSplitMost times the parts that all contexts at their
-// longest would give. Not split, 512-token pieces of eight 32768-token prompts (3.5
-// items an SM) take 1969 us back to back, in two parts each 1998.
-constexpr long long kSplitItems = 3, kSplitMost = 4;
-constexpr int kSplitTiles = 4;  // key tiles of a part, at least
+// call of few rows), unless they are shorter than two parts of 4 key tiles. The
+// device deals their key tiles to the SMs in equal shares. Not split, 512-token
+// pieces of eight 32768-token prompts (3.5 items an SM) take 1969 us back to back, in
+// two parts each 1998.
+constexpr long long kSplitItems = 3;
+constexpr int kSplitLeast = 8;  // key tiles of the longest context, at least
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
+// Tokens of the two tiles of rows of an item.
+int item_tokens(int num_heads, int num_kv_heads) { return pa::PF_NQ * pa::PF_BM / (num_heads / num_kv_heads); }
+
+// Items of the packed tokens of num_seqs sequences, at most: each sequence has at most one that is not full.
+long long max_items(int num_seqs, int num_tokens, int num_heads, int num_kv_heads) {
+    return (num_tokens / item_tokens(num_heads, num_kv_heads) + (long long)std::min(num_seqs, num_tokens)) *
+           num_kv_heads;
+}
+
 template <int D, typename T, bool PAGED>
-pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
+pa_status launch(pa::PrefillParams &p, cudaStream_t stream) {
     int dev, sms;
     pa_status st = pa_internal_device(&dev, &sms);
     if (st != PA_OK) return st;
@@ -93,17 +102,14 @@ pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         done[dev].store(true, std::memory_order_release);
     }
-    // Every sequence has at most one tile that is not full. Dealt key tiles: a CTA an SM.
-    const int tokens = pa::PF_NQ * pa::PF_BM / group;
-    const long long grid = max_parts > 1 ? sms
-                                         : (p.num_tokens / tokens + (long long)std::min(p.num_seqs, p.num_tokens)) *
-                                               p.num_kv_heads;
+    const long long grid =
+        p.deal ? p.deal_ctas : max_items(p.num_seqs, p.num_tokens, p.num_heads, p.num_kv_heads);
     if (grid >= (1ll << 31)) return fail(PA_ERR_UNSUPPORTED, "too many tiles");
     kernel<<<(unsigned)grid, SH::THREADS, SH::BYTES, stream>>>(p, maps);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, PAGED ? "pa_prefill_paged launch" : "pa_prefill launch");
     pa_internal_count_launch();
-    if (PAGED && max_parts > 1) {
+    if (PAGED && p.deal) {
         // Started early, it waits for the attention launch behind its own look-ups.
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(p.num_tokens * p.num_heads));
@@ -122,36 +128,40 @@ pa_status launch(pa::PrefillParams &p, int max_parts, cudaStream_t stream) {
 }
 
 template <bool PAGED>
-pa_status dispatch(pa::PrefillParams &p, int head_dim, int dtype, int max_parts, cudaStream_t s) {
+pa_status dispatch(pa::PrefillParams &p, int head_dim, int dtype, cudaStream_t s) {
     if (head_dim == 128)
-        return dtype == PA_F16 ? launch<128, __half, PAGED>(p, max_parts, s)
-                               : launch<128, __nv_bfloat16, PAGED>(p, max_parts, s);
-    return dtype == PA_F16 ? launch<64, __half, PAGED>(p, max_parts, s)
-                           : launch<64, __nv_bfloat16, PAGED>(p, max_parts, s);
+        return dtype == PA_F16 ? launch<128, __half, PAGED>(p, s) : launch<128, __nv_bfloat16, PAGED>(p, s);
+    return dtype == PA_F16 ? launch<64, __half, PAGED>(p, s) : launch<64, __nv_bfloat16, PAGED>(p, s);
 }
 
-// Parts that a context may be split into (1: it is not).
-int max_parts_of(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int max_keys, int sms) {
-    const long long rows = (long long)num_tokens * (num_heads / num_kv_heads);
-    if ((long long)num_tokens * num_heads >= (1ll << 31)) return 1;
-    const long long items =
-        std::max<long long>(std::min(num_seqs, num_tokens), ceil_div(rows, pa::PF_NQ * pa::PF_BM)) * num_kv_heads;
-    const int tiles = (int)ceil_div(max_keys, pa::PF_BN);
-    if (items >= kSplitItems * sms || tiles < 2 * kSplitTiles) return 1;
-    const long long least = std::max<long long>(kSplitTiles, ceil_div(items * tiles, kSplitMost * sms));
-    return (int)ceil_div(tiles - 1, least) + 2;
+// Whether a paged call's contexts are split.
+bool splits(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int max_keys, int sms) {
+    const long long items = std::max<long long>(std::min(num_seqs, num_tokens),
+                                                ceil_div(num_tokens, item_tokens(num_heads, num_kv_heads))) *
+                            num_kv_heads;
+    return items < kSplitItems * sms && ceil_div(max_keys, pa::PF_BN) >= kSplitLeast;
+}
+
+// Places for the parts of a split call: struct Deal. Each has room for an item's rows.
+long long part_slots(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int sms) {
+    return max_items(num_seqs, num_tokens, num_heads, num_kv_heads) + sms;
+}
+
+constexpr size_t kPartRows = pa::PF_NQ * pa::PF_BM;
+
+size_t parts_bytes(long long slots, int head_dim) {
+    return (size_t)slots * kPartRows * (sizeof(float2) + head_dim * sizeof(float));
 }
 
 template <bool PAGED>
-pa_status run(pa::PrefillParams &p, int max_parts, int head_dim, float scale, int dtype, cudaStream_t s) {
+pa_status run(pa::PrefillParams &p, int head_dim, float scale, int dtype, cudaStream_t s) {
     // A negative scale is a positive one of the negated queries (the matrix
     // instruction negates them); 0 stands for the least positive one, so that
     // a masked score of -inf stays -inf.
     const float a = fabsf(scale) * 1.4426950408889634f;
     p.scale_log2 = a < FLT_MIN ? FLT_MIN : a;
     p.negate = scale < 0.f;
-    p.max_parts = max_parts;
-    return dispatch<PAGED>(p, head_dim, dtype, max_parts, s);
+    return dispatch<PAGED>(p, head_dim, dtype, s);
 }
 
 bool heads_supported(int num_heads, int num_kv_heads) {
@@ -159,8 +169,6 @@ bool heads_supported(int num_heads, int num_kv_heads) {
     const int g = num_heads / num_kv_heads;
     return g == 1 || g == 2 || g == 4 || g == 8;
 }
-
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // What both entry points check before anything else.
 pa_status check_common(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim, float scale,
@@ -208,7 +216,7 @@ pa_status pa_prefill(void *out, const void *q, const void *k, const void *v, con
     p.k_stride = k_stride;
     p.v_stride = v_stride;
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
-    return run<false>(p, 1, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
+    return run<false>(p, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
 }
 
 size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
@@ -220,10 +228,11 @@ size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_hea
     if (num_seqs == 0 || num_tokens == 0) return 256;
     int dev, sms;
     if (pa_internal_device(&dev, &sms) != PA_OK) return 0;
-    const int parts = max_parts_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, sms);
-    if (parts == 1) return 256;
-    const size_t rows = (size_t)num_tokens * num_heads * parts;
-    return align256(rows * sizeof(float2)) + rows * head_dim * sizeof(float);
+    // Enough for every call that is no larger: one that splits has at most kSplitItems an SM
+    // of full items, and as many that are not full.
+    if (ceil_div(max_context_len, pa::PF_BN) < kSplitLeast) return 256;
+    const long long most = (2 * kSplitItems + 1) * sms;
+    return parts_bytes(std::min(part_slots(num_seqs, num_tokens, num_heads, num_kv_heads, sms), most), head_dim);
 }
 
 pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const void *v_pool,
@@ -248,9 +257,11 @@ pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const v
     if (q_stride % 8 || q_stride < (long long)num_heads * head_dim)
         return fail(PA_ERR_INVALID, "the token stride must be a multiple of 8 and hold a token's heads");
     if (workspace_bytes < 256) return fail(PA_ERR_INVALID, "workspace %zu bytes < 256", workspace_bytes);
-    const size_t need = pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
-                                                        block_size, max_context_len);
-    if (need == 0) return PA_ERR_CUDA;  // no device; pa_last_error() has the reason
+    int dev, sms;
+    if ((st = pa_internal_device(&dev, &sms)) != PA_OK) return st;
+    const bool deal = splits(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, sms);
+    const long long slots = deal ? part_slots(num_seqs, num_tokens, num_heads, num_kv_heads, sms) : 0;
+    const size_t need = deal ? parts_bytes(slots, head_dim) : 256;
     if (workspace_bytes < need)
         return fail(PA_ERR_INVALID, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     pa::PrefillParams p{};
@@ -272,14 +283,12 @@ pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, const v
     p.ctx_limit = (int)(table_tokens < max_context_len ? table_tokens : max_context_len);
     p.q_stride = q_stride;
     if ((st = pa_internal_error_word(&p.errors)) != PA_OK) return st;
-    int dev, sms;
-    if ((st = pa_internal_device(&dev, &sms)) != PA_OK) return st;
-    const int parts = max_parts_of(num_seqs, num_tokens, num_heads, num_kv_heads, max_context_len, sms);
-    p.sms = sms;
-    const size_t rows = (size_t)num_tokens * num_heads * parts;
+    p.deal = deal;
+    p.deal_ctas = sms;  // a CTA an SM
+    p.part_slots = (int)slots;
     p.part_ml = static_cast<float2 *>(workspace);
-    p.part_acc = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align256(rows * sizeof(float2)));
-    return run<true>(p, parts, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
+    p.part_acc = reinterpret_cast<float *>(p.part_ml + slots * kPartRows);
+    return run<true>(p, head_dim, scale, dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -84,24 +84,26 @@ __device__ __noinline__ RowPart<D> attend_row(const PrefillParams &p, int s, int
     return r;
 }
 
-// Stores what a warp has of a row: the output, or a part of a split context.
-template <int D, typename T>
-__device__ __forceinline__ void store_row(const PrefillParams &p, int row, int h, int part, int parts,
-                                          const RowPart<D> &r) {
+// Stores a part of a split context as row `at` of the parts.
+template <int D>
+__device__ __forceinline__ void store_part(const PrefillParams &p, size_t at, const RowPart<D> &r) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
-    size_t at = (size_t)row * p.num_heads + h;
-    if (parts > 1) {
-        at += (size_t)part * p.num_tokens * p.num_heads;
 #pragma unroll
-        for (int e = 0; e < E; ++e) p.part_acc[at * D + lane * E + e] = r.acc[e];
-        if (lane == 0) p.part_ml[at] = make_float2(r.m, r.l);
-    } else {
-        const float inv = 1.f / r.l;  // scores that are all -inf give 0 / 0
-        uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at * D) + lane * (E / 2);
+    for (int e = 0; e < E; ++e) p.part_acc[at * D + lane * E + e] = r.acc[e];
+    if (lane == 0) p.part_ml[at] = make_float2(r.m, r.l);
+}
+
+// Stores a row's output.
+template <int D, typename T>
+__device__ __forceinline__ void store_row(const PrefillParams &p, int row, int h, const RowPart<D> &r) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const size_t at = (size_t)row * p.num_heads + h;
+    const float inv = 1.f / r.l;  // scores that are all -inf give 0 / 0
+    uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at * D) + lane * (E / 2);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) out[e] = Elem<T>::pack(r.acc[2 * e] * inv, r.acc[2 * e + 1] * inv);
-    }
+    for (int e = 0; e < E / 2; ++e) out[e] = Elem<T>::pack(r.acc[2 * e] * inv, r.acc[2 * e + 1] * inv);
 }
 
 }  // namespace pa

@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
         it.row0 = __shfl_sync(FULL_MASK, at[2], 0);
         it.n = __shfl_sync(FULL_MASK, at[3], 0);
         it.keys = __shfl_sync(FULL_MASK, at[4], 0);
-        it.part = __shfl_sync(FULL_MASK, at[5], 0);
+        it.slot = __shfl_sync(FULL_MASK, at[5], 0);
         it.parts = __shfl_sync(FULL_MASK, at[6], 0);
         it.kvh = __shfl_sync(FULL_MASK, at[7], 0);
         it.j0 = __shfl_sync(FULL_MASK, at[8], 0);
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             unsigned bad = 0;
             for (int nth = 0;; ++nth) {
                 Item it;
-                const bool deal = PAGED && p.max_parts > 1;
+                const bool deal = PAGED && p.deal;
                 const bool work = deal ? finder.next_piece(p, NQ * tm, it, bad)
                                        : index >= 0 && finder.find(p, index, NQ * tm, it, bad);
                 if (!work) it.s = -1;
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                     at[2] = it.row0;
                     at[3] = it.n;
                     at[4] = it.keys;
-                    at[5] = it.part;
+                    at[5] = it.slot;
                     at[6] = it.parts;
                     at[7] = it.kvh;
                     at[8] = it.j0;
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             results0 += w.count[0] > 0;
             results1 += w.count[1] > 0;
             const size_t at = (size_t)(it.row0 + tok) * p.num_heads + head;
-            const size_t part_at = (size_t)it.part * p.num_tokens * p.num_heads + at;
+            const size_t part_at = (size_t)it.slot * (NQ * PF_BM) + (tok0 - it.tok0) * group + r;
             float2 nan[4] = {};  // 0 as long as all that goes in is finite
             const uint32_t other_addr = w.halves ? o_addr + D : o_addr;  // not in halves: f1 is 0
 #pragma unroll 1
@@ -819,7 +819,10 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                 const int row = it.row0 + __shfl_sync(FULL_MASK, tok, src), h = __shfl_sync(FULL_MASK, head, src);
                 const RowPart<D> part =
                     attend_row<D, T, PAGED>(p, it.s, it.row0, row, h, lo, __shfl_sync(FULL_MASK, hi, src));
-                store_row<D, T>(p, row, h, it.part, it.parts, part);
+                if (PAGED && it.parts > 1)
+                    store_part<D>(p, __shfl_sync(FULL_MASK, part_at, src), part);
+                else
+                    store_row<D, T>(p, row, h, part);
             }
         }
     }
@@ -850,42 +853,43 @@ __global__ void __launch_bounds__(128) pa_prefill_join_kernel(const __grid_const
             hi = mid;
     }
     // The parts of its chain, from all sequences' chains.
-    __shared__ long long sums[4][2];
+    __shared__ long long sums[4][3];
     __shared__ int most[4];
     unsigned bad = 0;
-    const int group = p.num_heads / p.num_kv_heads, TM = PF_NQ * PF_BM / group;
-    long long sum = 0, before = 0;
+    const int TM = PF_NQ * PF_BM / (p.num_heads / p.num_kv_heads);
+    long long sum = 0, before = 0, chains_before = 0;
     int longest = 1;
     for (int s = threadIdx.x; s < p.num_seqs; s += 128) {
-        const Deal d = Deal::of<true>(p, seq_range<true>(p, s, bad), TM);
+        const Deal d = Deal::of(seq_range<true>(p, s, bad), TM);
         sum += d.all(p);
         before += s < lo ? d.all(p) : 0;
+        chains_before += s < lo ? (long long)d.chains * p.num_kv_heads : 0;
         if (d.chains > 0) longest = max(longest, d.tiles);
     }
     sum = warp_sum(sum);
     before = warp_sum(before);
+    chains_before = warp_sum(chains_before);
     longest = __reduce_max_sync(FULL_MASK, longest);
-    if (lane == 0) sums[warp][0] = sum, sums[warp][1] = before, most[warp] = longest;
+    if (lane == 0) sums[warp][0] = sum, sums[warp][1] = before, sums[warp][2] = chains_before, most[warp] = longest;
     __syncthreads();
     sum = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
     before = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
+    chains_before = sums[0][2] + sums[1][2] + sums[2][2] + sums[3][2];
     longest = max(max(most[0], most[1]), max(most[2], most[3]));
     const SeqRange r = seq_range<true>(p, lo, bad);
-    const Deal d = Deal::of<true>(p, r, TM);
-    const long long share = Deal::share_of(p, sum, longest);
-    const int chain = (item % p.num_heads) / group * d.chains + (row - r.row0) / TM;
-    const long long start = before + (long long)chain * d.tiles;
-    const int parts = (int)((start + d.tiles - 1) / share - start / share) + 1;
+    const bool inside = row >= r.row0 && row < r.row0 + r.n;
+    const RowParts w = parts_of_row(p, r, inside ? row - r.row0 : 0, item % p.num_heads, TM,
+                                    Deal::share_of(sum, longest, p.deal_ctas), before, chains_before);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention launch before this one is done
-    if (row < r.row0 || row >= r.row0 + r.n || parts == 1) return;
-    const size_t stride = (size_t)p.num_tokens * p.num_heads;
+    if (!inside || w.parts == 1) return;
     float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int i = warp; i < parts; i += 4) {
-        const float2 ml = p.part_ml[i * stride + item];
-        const float *a = p.part_acc + (i * stride + item) * D + lane * E;
+    for (int i = warp; i < w.parts; i += 4) {
+        const size_t at = (size_t)min(w.slot + i, p.part_slots - 1) * (PF_NQ * PF_BM) + w.row;
+        const float2 ml = p.part_ml[at];
+        const float *a = p.part_acc + at * D + lane * E;
         float x[E];
         if constexpr (E == 4) {
             const float4 v = *reinterpret_cast<const float4 *>(a);

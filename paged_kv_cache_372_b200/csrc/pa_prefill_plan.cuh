@@ -22,9 +22,11 @@ struct PrefillParams {
     long long q_stride, k_stride, v_stride;                     // elements from token to token
     float scale_log2;                                           // |scale| * log2(e), above 0
     bool negate;                                                // the scale is -scale_log2
-    int sms, max_parts;  // parts that a context may be split into (paged), 1: it is not
-    float *part_acc;   // [part][token][head][head_dim]: weighted values of the parts
-    float2 *part_ml;   // [part][token][head]: what they are relative to (log2), sum of the weights
+    bool deal;         // whether contexts are split (paged; struct Deal)
+    int deal_ctas;     // CTAs that share the key tiles then
+    int part_slots;    // places for parts of a chain
+    float *part_acc;   // [slot][row of the chain][head_dim]: weighted values of the parts
+    float2 *part_ml;   // [slot][row of the chain]: what they are relative to (log2), sum of the weights
     unsigned int *errors;
 };
 
@@ -52,7 +54,7 @@ __device__ __forceinline__ SeqRange seq_range(const PrefillParams &p, int s, uns
 struct Item {
     int s, tok0;           // sequence, first token of the tile among its rows
     int row0, n, keys;     // as SeqRange
-    int part, parts, kvh;  // part of the context and their number, KV head
+    int slot, parts, kvh;  // the part's place, how many parts the chain has, KV head
     int j0, j1;            // key tiles of the part, where there are more than one
 };
 
@@ -97,24 +99,31 @@ __device__ __forceinline__ Walk walk_of(const Item &it, int tm, bool halves) {
 
 // Few rows over long contexts: the key tiles of all (sequence, KV head, tile of
 // rows), a chain each and the chains one after the other, are dealt to the CTAs
-// in equal shares, cut where a share ends. A chain's parts are the shares it touches.
+// in equal shares, cut where a share ends. A chain's parts are the shares it
+// touches. The part of the chain with index c that CTA b walks has the place c + b:
+// of two parts that follow one another the later has the next chain, the next CTA
+// or both, so no place is used twice and all lie below chains + CTAs.
 struct Deal {
-    long long share;
     int chains, tiles;  // of a sequence: chains of a KV head, key tiles of a chain
 
-    template <bool PAGED>
-    __device__ __forceinline__ static Deal of(const PrefillParams &p, const SeqRange &r, int TM) {
-        return Deal{0, (r.n + TM - 1) / TM, max((r.keys + PF_BN - 1) / PF_BN, 1)};
+    __device__ __forceinline__ static Deal of(const SeqRange &r, int TM) {
+        return Deal{(r.n + TM - 1) / TM, max((r.keys + PF_BN - 1) / PF_BN, 1)};
     }
     // Key tiles of a sequence's chains.
     __device__ __forceinline__ long long all(const PrefillParams &p) const {
         return (long long)chains * tiles * p.num_kv_heads;
     }
-    // An equal share, but no chain in more parts than there is room for, nor in parts of less than 4.
-    __device__ __forceinline__ static long long share_of(const PrefillParams &p, long long sum, int longest) {
-        const long long even = (sum + p.sms - 1) / p.sms;
-        const int room = (longest - 1 + p.max_parts - 3) / (p.max_parts - 2);
-        return max(even, (long long)max(room, min(longest, 4)));
+    // An equal share, but no chain in parts of less than 4. sum: all key tiles, longest: of a chain.
+    __device__ __forceinline__ static long long share_of(long long sum, int longest, int ctas) {
+        return max((sum + ctas - 1) / ctas, (long long)min(longest, 4));
+    }
+    // Parts of a chain whose first key tile is number `start` of all.
+    __device__ __forceinline__ int parts(long long start, long long share) const {
+        return (int)((start + tiles - 1) / share - start / share) + 1;
+    }
+    // Place of a part; boundaries that overlap (flagged) can make more chains than there is room for.
+    __device__ __forceinline__ static int slot(const PrefillParams &p, long long chain, long long cta) {
+        return (int)min(chain + cta, (long long)p.part_slots - 1);
     }
 };
 
@@ -166,44 +175,51 @@ struct Finder {
             long long sum = 0;
             int longest = 1;
             for (int s = lane; s < B; s += 32) {
-                const Deal d = Deal::of<PAGED>(p, seq_range<PAGED>(p, s, bad), TM);
+                const Deal d = Deal::of(seq_range<PAGED>(p, s, bad), TM);
                 sum += d.all(p);
                 if (d.chains > 0) longest = max(longest, d.tiles);
             }
             sum = warp_sum(sum);
-            share = Deal::share_of(p, sum, __reduce_max_sync(FULL_MASK, longest));
+            share = Deal::share_of(sum, __reduce_max_sync(FULL_MASK, longest), p.deal_ctas);
             at = min(share * blockIdx.x, sum);
             end = min(at + share, sum);
         }
         if (at >= end) return false;
-        long long before = 0;
+        long long before = 0, chains_before = 0;
         for (int s0 = 0; s0 < B; s0 += 32) {
-            Deal d{0, 0, 1};
-            if (s0 + lane < B) d = Deal::of<PAGED>(p, seq_range<PAGED>(p, s0 + lane, bad), TM);
-            long long sum = d.all(p);
+            Deal d{0, 1};
+            if (s0 + lane < B) d = Deal::of(seq_range<PAGED>(p, s0 + lane, bad), TM);
+            long long sum = d.all(p), chains_sum = (long long)d.chains * p.num_kv_heads;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long up = __shfl_up_sync(FULL_MASK, sum, o);
-                if (lane >= o) sum += up;
+                const long long chains_up = __shfl_up_sync(FULL_MASK, chains_sum, o);
+                if (lane >= o) {
+                    sum += up;
+                    chains_sum += chains_up;
+                }
             }
             const unsigned m = __ballot_sync(FULL_MASK, before + sum > at);
             if (m) {
                 const int src = __ffs(m) - 1;
-                const int chains = __shfl_sync(FULL_MASK, d.chains, src), tiles_of = __shfl_sync(FULL_MASK, d.tiles, src);
-                const long long in = at - before - __shfl_sync(FULL_MASK, sum - d.all(p), src);
-                const int chain = (int)(in / tiles_of);
-                it.j0 = (int)(in % tiles_of);
-                const long long start = at - it.j0;
-                it.part = (int)(blockIdx.x - start / share);
-                it.parts = (int)((start + tiles_of - 1) / share - start / share) + 1;
-                it.j1 = (int)min((long long)tiles_of, it.j0 + (end - at));
-                it.kvh = chain / chains;
-                it.tok0 = chain % chains * TM;
+                d.chains = __shfl_sync(FULL_MASK, d.chains, src);
+                d.tiles = __shfl_sync(FULL_MASK, d.tiles, src);
+                const long long in = at - before - (__shfl_sync(FULL_MASK, sum, src) - d.all(p));
+                const int chain = (int)(in / d.tiles);
+                it.j0 = (int)(in % d.tiles);
+                const long long first_chain =
+                    chains_before + __shfl_sync(FULL_MASK, chains_sum, src) - (long long)d.chains * p.num_kv_heads;
+                it.slot = Deal::slot(p, first_chain + chain, blockIdx.x);
+                it.parts = d.parts(at - it.j0, share);
+                it.j1 = (int)min((long long)d.tiles, it.j0 + (end - at));
+                it.kvh = chain / d.chains;
+                it.tok0 = chain % d.chains * TM;
                 take(p, s0 + src, it, bad);
                 at += it.j1 - it.j0;
                 return true;
             }
             before += __shfl_sync(FULL_MASK, sum, 31);
+            chains_before += __shfl_sync(FULL_MASK, chains_sum, 31);
         }
         return false;
     }
@@ -275,7 +291,7 @@ struct Finder {
                 last = __shfl_sync(FULL_MASK, last, src);
                 it.kvh = in / (last - first);
                 it.tok0 = (last - 1 - in % (last - first)) * TM;
-                it.part = it.j0 = it.j1 = 0;
+                it.slot = it.j0 = it.j1 = 0;
                 it.parts = 1;
                 take(p, s0 + src, it, bad);
                 return true;
@@ -285,5 +301,22 @@ struct Finder {
         return false;
     }
 };
+
+// Where a row's parts lie: places slot .. slot + parts - 1, the row's number in each.
+struct RowParts {
+    int slot, parts, row;
+};
+
+// Of row `token` (from the sequence's first) of head h in sequence s. before,
+// chains_before: key tiles and chains of the sequences before s.
+__device__ __forceinline__ RowParts parts_of_row(const PrefillParams &p, const SeqRange &r, int token, int h, int TM,
+                                                 long long share, long long before, long long chains_before) {
+    const int group = p.num_heads / p.num_kv_heads;
+    const Deal d = Deal::of(r, TM);
+    const int chain = h / group * d.chains + token / TM;
+    const long long start = before + (long long)chain * d.tiles;
+    return RowParts{Deal::slot(p, chains_before + chain, start / share), d.parts(start, share),
+                    token % TM * group + h % group};
+}
 
 }  // namespace pa

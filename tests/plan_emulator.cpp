@@ -150,23 +150,66 @@ static void find_items(const std::vector<int> &order) {
                items[i].row0, items[i].n, items[i].keys);
 }
 
+// The pieces that each CTA walks where contexts are split, and where the rows' parts lie.
+static void deal() {
+    for (int cta = 0; cta < params.deal_ctas; ++cta) {
+        std::vector<pa::Item> items;
+        unsigned bads[32] = {};
+        blockIdx.x = cta;
+        emu::run_warp([&] {
+            pa::Finder<true> finder;
+            const int lane = threadIdx.x;
+            pa::Item it = {};
+            while (finder.next_piece(params, TM, it, bads[lane]))
+                if (lane == 0) items.push_back(it);
+        });
+        for (const pa::Item &it : items)
+            printf("1 %d %d %d %d %d %d %d %d\n", cta, it.s, it.tok0, it.kvh, it.j0, it.j1, it.slot, it.parts);
+    }
+    unsigned bad = 0;
+    long long sum = 0, before = 0, chains_before = 0;
+    int longest = 1;
+    std::vector<pa::SeqRange> rows;
+    for (int s = 0; s < params.num_seqs; ++s) {
+        rows.push_back(pa::seq_range<true>(params, s, bad));
+        const pa::Deal d = pa::Deal::of(rows[s], TM);
+        sum += d.all(params);
+        if (d.chains > 0) longest = max(longest, d.tiles);
+    }
+    const long long share = pa::Deal::share_of(sum, longest, params.deal_ctas);
+    for (int s = 0; s < params.num_seqs; ++s) {
+        for (int i = 0; i < rows[s].n; ++i)
+            for (int h = 0; h < params.num_heads; ++h) {
+                const pa::RowParts r = pa::parts_of_row(params, rows[s], i, h, TM, share, before, chains_before);
+                printf("2 %d %d %d %d %d %d\n", s, i, h, r.slot, r.parts, r.row);
+            }
+        const pa::Deal d = pa::Deal::of(rows[s], TM);
+        before += d.all(params);
+        chains_before += (long long)d.chains * params.num_kv_heads;
+    }
+}
+
 int main() {
     char what[16];
     while (scanf("%15s", what) == 1) {
-        // paged, sequences, tokens, heads, KV heads, limit of a context, SMs, count of indices
-        const std::vector<int> a = numbers(8);
-        const std::vector<int> cu = numbers(a[1] + 1), ctx = numbers(a[1]), order = numbers(a[7]);
+        // paged, sequences, tokens, heads, KV heads, limit of a context, CTAs and slots of a deal, count of indices
+        const std::vector<int> a = numbers(9);
+        const std::vector<int> cu = numbers(a[1] + 1), ctx = numbers(a[1]), order = numbers(a[8]);
         params = pa::PrefillParams{};
         params.num_seqs = a[1];
         params.num_tokens = a[2];
         params.num_heads = a[3];
         params.num_kv_heads = a[4];
         params.ctx_limit = a[5];
-        params.sms = a[6];
+        params.deal_ctas = a[6];
+        params.part_slots = a[7];
         params.cu_seqlens = cu.data();
         params.context_lens = ctx.data();
         TM = pa::PF_NQ * pa::PF_BM / (a[3] / a[4]);
-        a[0] ? find_items<true>(order) : find_items<false>(order);
+        if (what[0] == 'd')
+            deal();
+        else
+            a[0] ? find_items<true>(order) : find_items<false>(order);
         printf("end\n");
         fflush(stdout);
     }

@@ -51,3 +51,39 @@ def test_decodes_without_a_workspace_on_the_current_and_on_another_stream(call):
             # partitions may merge in any order: 32-bit sums, one rounding to the type
             want = calls[i % 2][1].float()
             assert ((out.float() - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("H,Hkv,D", [(32, 8, 128), (8, 1, 64), (4, 4, 128)])
+def test_prefill_workspace_size_grows_with_every_size(H, Hkv, D):
+    def size(b, t, c):
+        return pa.pa_prefill_paged_workspace_size(b, t, H, Hkv, D, 16, c)
+
+    seqs, tokens, limits = (1, 2, 8, 16, 64, 400), (1, 3, 16, 64, 500, 2048, 4096, 9000), (40, 1000, 1024, 2944, 32768)
+    for b in seqs:
+        for t in tokens:
+            for c in limits:
+                n = size(b, t, c)
+                assert 256 <= n <= 138 << 20
+                assert all(size(*x) <= n for x in ((b - 1, t, c), (b, t - 1, c), (b, t, c - 1), (1, t, c), (b, 1, c)))
+
+
+def test_a_workspace_for_the_largest_sizes_serves_smaller_calls():
+    H, Hkv, D, bs, most = 8, 2, 128, 16, (64, 9000, 8192)
+    ws = pa.alloc_prefill_workspace(most[0], most[1], H, Hkv, D, bs, most[2])
+    for ctx, new in [([8000], [1]), ([40], [40]), ([3000, 5, 8192], [8, 5, 700]), ([1100] * 64, [3] * 64),
+                     ([8192, 808], [8192, 808])]:
+        q, kp, vp, table, cu = pooled(ctx, new, H, Hkv, D, bs, torch.bfloat16, 70)
+        ws.fill_(255)
+        for limit in (max(ctx), most[2]):
+            run_paged(q, kp, vp, table, ctx, cu, 0.1, limit, ws)
+
+
+def test_a_workspace_too_small_for_its_call_is_refused():
+    ctx, new = [3000], [8]
+    q, kp, vp, table, cu = pooled(ctx, new, 8, 2, 128, 16, torch.bfloat16, 71)
+    out = torch.full_like(q, 7.0)
+    n = pa.pa_prefill_paged_workspace_size(1, q.shape[0], 8, 2, 128, 16, 3000)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    with pytest.raises(pa.PagedAttentionError) as e:
+        pa.pa_prefill_paged(out, q, kp, vp, table, ints(ctx), ints(cu), 0.1, 3000, ws[:n - 256])
+    assert e.value.status == pa.PA_ERR_INVALID and (out == 7.0).all()
