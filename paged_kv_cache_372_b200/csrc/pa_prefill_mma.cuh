@@ -54,6 +54,11 @@ namespace pa {
 // LLaMA-7B-shaped prompts, fp16, 199 / 192 / 190 / 195.
 template <int D>
 constexpr int PF_POLY = D == 64 ? 4 : 5;
+// What the weights are relative to, m * scale_log2, is rounded to 32 bits: a row's weights all carry a factor, up
+// to 2^(1/4) at the size below, which cancels. It grows with the scores (2^32 at 2^30), until the weights leave fp16's
+// range or ex2_fma's. Rows whose maximum has been past this size are computed again by the row form, which
+// subtracts the maximum from the scaled scores.
+constexpr float PF_COARSE = 4194304.f;  // 2^22
 constexpr uint64_t PF_WAIT_NS = 4000000000ull;
 
 template <int D>
@@ -633,6 +638,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             // Keys that all of the warp's rows see.
             const int clear = max(w.first + tok0 + (r - lane) / group + 1, 0);
             float m = -INFINITY, l = 0.f;  // m: what the weights are relative to, unscaled
+            bool coarse = false;           // m has been past PF_COARSE
             for (int j = 0; j < mine; ++j) {
                 if (!wait(s_full(t), scores & 1)) break;
                 ++scores;
@@ -665,6 +671,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                 if (__any_sync(FULL_MASK, grow)) {
                     const float f = grow ? ex2((m - top) * p.scale_log2) : 1.f;
                     m = grow ? top : m;
+                    coarse = coarse || (fabsf(m) * p.scale_log2 >= PF_COARSE && fabsf(m) < INFINITY);
                     l *= f;
                     if (j > 0) {
 #pragma unroll 1
@@ -719,7 +726,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             if (w.halves) {
                 float2 *swap = reinterpret_cast<float2 *>(smem + SH::OFF_SWAP) + r;
                 if (t == 1) {
-                    *swap = make_float2(m, l);
+                    *swap = make_float2(m, coarse ? -1.f : l);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(pair_full);
                     if (!wait(pair_empty, pairs & 1)) break;
@@ -731,6 +738,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                 if (!wait(pair_full, pairs & 1) || !wait(o_full(1), results1 & 1)) break;
                 ++pairs;
                 const float2 other = *swap;
+                coarse = coarse || other.y < 0.f;
                 const float top = fmaxf(m, other.x);
                 f0 = m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
                 f1 = other.x == -INFINITY ? 0.f : ex2((other.x - top) * p.scale_log2);
@@ -742,7 +750,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                 f0 *= inv;
                 f1 *= inv;
             }
-            bool again = some && !(l > 0.f && l < INFINITY);
+            bool again = some && (coarse || !(l > 0.f && l < INFINITY));
             if (mine > 0) {
                 if (!wait(o_full(t), (t == 0 ? results0 : results1) & 1)) break;
                 tc_fence_after();

@@ -1,0 +1,71 @@
+"""Prompt attention on scores and values far from the ordinary: scores that 32 bits hold to whole numbers only, weights
+far below the largest, values near the type's largest, infinities and NaN."""
+import pytest
+import torch
+
+import paged_kv_cache_372_b200 as pa
+from tests import prompt_reference as ref
+from tests.test_gpu_prompt_path import bits, check, gen, ints, normal, run_packed, run_paged
+
+pytestmark = pytest.mark.gpu
+
+U = ref.U
+
+
+def one_pool(k, v, bs):
+    """k, v [m][Hkv][D] as the blocks of one sequence, in order."""
+    m, Hkv, D = k.shape
+    nb = -(-m // bs)
+    kp, vp = (torch.zeros((nb * bs, Hkv, D), dtype=k.dtype, device="cuda") for _ in range(2))
+    kp[:m], vp[:m] = k, v
+    kp, vp = (x.view(nb, bs, Hkv, D).transpose(1, 2).contiguous() for x in (kp, vp))
+    return kp, vp, ints([list(range(nb))])
+
+
+def equal_scores(n, rows, H, Hkv, D, dtype, a, seed):
+    """Every score of the last rows is the same: a^2 D scale, exactly; the weights are equal."""
+    q = torch.full((rows, H, D), a, dtype=dtype, device="cuda")
+    k = torch.full((n, Hkv, D), a, dtype=dtype, device="cuda")
+    return q, k, normal((n, Hkv, D), dtype, gen(seed))
+
+
+# Powers of two, so that every product and sum of the scores is exact; the scaled score has 2^20 to 2^61.
+SIZES = [(torch.float16, 2.0 ** 9), (torch.float16, 2.0 ** 11), (torch.float16, 2.0 ** 13), (torch.float16, 2.0 ** 14.5 // 1),
+         (torch.bfloat16, 2.0 ** 13), (torch.bfloat16, 2.0 ** 16), (torch.bfloat16, 2.0 ** 28)]
+
+
+@pytest.mark.parametrize("dtype,a", SIZES, ids=lambda x: str(x))
+@pytest.mark.parametrize("H,Hkv,D", [(2, 2, 64), (4, 1, 128)])
+@pytest.mark.parametrize("scale", [0.0912, -0.0912])
+def test_equal_scores_of_any_size_weigh_equally(dtype, a, H, Hkv, D, scale):
+    n = 300
+    q, k, v = equal_scores(n, n, H, Hkv, D, dtype, a, 80)
+    out = run_packed(q, k, v, [0, n], scale, compare=False)
+    rows = torch.arange(1, n + 1, device="cuda", dtype=torch.float64)[:, None, None]
+    mean = (v.double().cumsum(0) / rows).repeat_interleave(H // Hkv, 1)
+    size = (v.double().abs().cumsum(0) / rows).repeat_interleave(H // Hkv, 1)
+    # its rounding, the weights' rounding to the type, 32-bit sums of n products
+    bound = U[dtype] * mean.abs() + (U[dtype] + 2 * n * 2.0 ** -24) * size + 2.0 ** -25
+    check(out, mean, bound)
+
+
+@pytest.mark.parametrize("dtype,a", SIZES, ids=lambda x: str(x))
+@pytest.mark.parametrize("n,rows", [(2500, 3), (700, 300)])
+def test_one_score_above_many_equal_ones_of_any_size(dtype, a, n, rows):
+    # the largest key's score is a quarter above the others': it takes all of the weight
+    q, k, v = equal_scores(n, rows, 4, 2, 128, dtype, a, 81)
+    at = n - rows // 2 - 1
+    k[at] *= 1.25
+    kp, vp, table = one_pool(k, v, 16)
+    out = torch.full_like(q, 7.0)
+    pa.pa_prefill_paged(out, q, kp, vp, table, ints([n]), ints([0, rows]), 0.0912, n)
+    assert pa.pa_device_errors() == 0
+    sees = n - rows + torch.arange(rows, device="cuda") >= at
+    assert torch.equal(bits(out[sees]), bits(v[at].repeat_interleave(2, 0).expand(int(sees.sum()), 4, 128)))
+    i = torch.arange(n, device="cuda")[None, :, None, None]
+    seen = (i <= n - rows + torch.arange(rows, device="cuda")[:, None, None, None])[~sees]
+    count = seen.sum(1)
+    mean = (seen * v.double()[None]).sum(1) / count
+    size = (seen * v.double().abs()[None]).sum(1) / count
+    bound = U[dtype] * mean.abs() + (U[dtype] + 2 * n * 2.0 ** -24) * size + 2.0 ** -25
+    check(out[~sees], mean.repeat_interleave(2, 1), bound.repeat_interleave(2, 1))
