@@ -5,12 +5,13 @@
 // of the group, head fastest: all query heads of a KV head share its key and value
 // tiles, and a tile spans few tokens, so little of it is masked. For each tile
 //   S = Q K^T      tcgen05.mma, both operands in shared memory, S in TMEM
-//   P = exp2(S * scale_log2 - m)   a thread for each row, in registers; P rounded
-//                  to the input type goes back to TMEM over S
+//   P = exp2(S * scale_log2 - m + lift)   a thread for each row, in registers; P
+//                  rounded to the input type goes back to TMEM over S
 //   O += P V       tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
 // m is a running maximum of the row and l the running sum, both 32 bits; O and
-// l are rescaled only when the maximum has grown by more than 2^8 (P then stays
-// below 2^8, far inside fp16's range), which after the first tiles is rare.
+// l are rescaled only when the maximum has grown by more than 2^8 (P 2^-lift then
+// stays below 2^8), which after the first tiles is rare. P is rounded since the
+// products take one type; the sum l is of the weights before that rounding.
 //
 // Warps: four softmax warps for each tile of rows, one that issues the copies
 // (TMA), one for each tile of rows that issues its matrix instructions, and one
@@ -59,6 +60,12 @@ constexpr int PF_POLY = D == 64 ? 4 : 5;
 // range or ex2_fma's. Rows whose maximum has been past this size are computed again by the row form, which
 // subtracts the maximum from the scaled scores.
 constexpr float PF_COARSE = 4194304.f;  // 2^22
+// Weights are lifted to where the type has room. fp16: by 2^7, so that the largest
+// (2^15 and the factor above) is just below 65504 and rounding is to 2^-32 of the
+// largest, not 2^-25: long contexts of small weights add up. bf16, whose range has
+// room below: by 2^-8, so that none is above 1 and sums of values overflow no sooner.
+template <typename T>
+constexpr float PF_LIFT = std::is_same<T, __half>::value ? 7.f : -8.f;
 constexpr uint64_t PF_WAIT_NS = 4000000000ull;
 
 template <int D>
@@ -253,7 +260,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // [-1/2, 1/2] with the constant term 1 (a linear programme over 4001 points):
 // 1.0e-4 of degree 3 for bf16, whose weights are rounded to 2^-9, 2.9e-6 of degree
 // 4 for fp16. x below -127 counts as -127, whose f is 0 and whose result is 0.
-// x up to 127; a NaN gives a weight so large that the row's sums overflow.
+// x up to 16; a NaN gives a weight so large that the row's sums overflow.
 template <typename T>
 __device__ __forceinline__ float2 ex2_fma(float2 x) {
     x.x = max_nan(x.x, -127.f);
@@ -685,7 +692,8 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.f : -m * p.scale_log2;  // nothing above -inf yet: weights 0
+                // nothing above -inf yet: weights 0
+                const float ref = m == -INFINITY ? 0.f : fmaf(-m, p.scale_log2, PF_LIFT<T>);
                 const float2 ref2 = make_float2(ref, ref);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 auto weigh = [&](int c) {
@@ -807,7 +815,8 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                 __syncwarp();
             }
             if (PAGED && it.parts > 1 && valid)
-                p.part_ml[part_at] = make_float2(some ? m * p.scale_log2 : -INFINITY, some ? l : 0.f);
+                p.part_ml[part_at] =
+                    make_float2(some ? -fmaf(-m, p.scale_log2, PF_LIFT<T>) : -INFINITY, some ? l : 0.f);
             if (valid && !some) {  // a row that sees nothing here: zeros, over what is in its place
                 const uint32_t none[8] = {};
                 if (PAGED && it.parts > 1) {

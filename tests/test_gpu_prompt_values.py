@@ -69,3 +69,34 @@ def test_one_score_above_many_equal_ones_of_any_size(dtype, a, n, rows):
     size = (seen * v.double().abs()[None]).sum(1) / count
     bound = U[dtype] * mean.abs() + (U[dtype] + 2 * n * 2.0 ** -24) * size + 2.0 ** -25
     check(out[~sees], mean.repeat_interleave(2, 1), bound.repeat_interleave(2, 1))
+
+
+@pytest.mark.parametrize("n,rows", [(40000, 2), (9000, 300)])
+def test_many_weights_far_below_the_largest_add_up_in_fp16(n, rows):
+    # the first key takes nearly all of the weight and has the value 0; each other one has e^-18, below 2^-25
+    q = torch.zeros((rows, 2, 64), dtype=torch.float16, device="cuda")
+    k = torch.zeros((n, 1, 64), dtype=torch.float16, device="cuda")
+    v = torch.ones((n, 1, 64), dtype=torch.float16, device="cuda")
+    q[..., 0], k[0, :, 0], v[0] = 1.0, 18.0, 0.0
+    kp, vp, table = one_pool(k, v, 64)
+    out = torch.full_like(q, 7.0)
+    pa.pa_prefill_paged(out, q, kp, vp, table, ints([n]), ints([0, rows]), 1.0, n)
+    assert pa.pa_device_errors() == 0
+    rest = (n - rows + torch.arange(rows, device="cuda", dtype=torch.float64)) * torch.exp(torch.tensor(-18.0).double())
+    want = (rest / (1 + rest))[:, None, None].expand(out.shape)
+    # its rounding; each weight is off by 2^-25 of 2^7 times the largest; 32-bit sums and exponentials (2^-17)
+    check(out, want, 2.0 ** -11 * want + n * 2.0 ** -32 + 2.0 ** -17 * want)
+
+
+@pytest.mark.parametrize("n,rows", [(300, 300), (1500, 4)])
+def test_sums_of_values_near_the_largest_of_bf16(n, rows):
+    q = torch.zeros((rows, 4, 128), dtype=torch.bfloat16, device="cuda")
+    k = normal((n, 2, 128), torch.bfloat16, gen(82))
+    v = torch.full((n, 2, 128), 2.0 ** 120, dtype=torch.bfloat16, device="cuda")
+    kp, vp, table = one_pool(k, v, 32)
+    out = torch.full_like(q, 7.0)
+    pa.pa_prefill_paged(out, q, kp, vp, table, ints([n]), ints([0, rows]), 0.1, n)
+    assert pa.pa_device_errors() == 0
+    assert (out == 2.0 ** 120).all()
+    if n == rows:
+        assert (run_packed(q, k, v, [0, n], 0.1, compare=False) == 2.0 ** 120).all()
