@@ -153,6 +153,12 @@ size_t parts_bytes(long long slots, int head_dim) {
     return (size_t)slots * kPartRows * (sizeof(float2) + head_dim * sizeof(float));
 }
 
+// The limit of a wait: 4 s, and for each key that a row may see the time that the
+// 32 rows of a warp take for it one after the other in the row form (100 ns each
+// with the keys in L2, three times that allowed), since the other warps wait
+// meanwhile for this item's end.
+unsigned long long wait_limit_ns(int max_keys) { return 4000000000ull + 10000ull * max_keys; }
+
 template <bool PAGED>
 pa_status run(pa::PrefillParams &p, int head_dim, float scale, int dtype, cudaStream_t s) {
     // A negative scale is a positive one of the negated queries (the matrix
@@ -161,6 +167,7 @@ pa_status run(pa::PrefillParams &p, int head_dim, float scale, int dtype, cudaSt
     const float a = fabsf(scale) * 1.4426950408889634f;
     p.scale_log2 = a < FLT_MIN ? FLT_MIN : a;
     p.negate = scale < 0.f;
+    p.wait_ns = wait_limit_ns(PAGED ? p.ctx_limit : p.num_tokens);
     return dispatch<PAGED>(p, head_dim, dtype, s);
 }
 

@@ -66,7 +66,6 @@ constexpr float PF_COARSE = 4194304.f;  // 2^22
 // room below: by 2^-8, so that none is above 1 and sums of values overflow no sooner.
 template <typename T>
 constexpr float PF_LIFT = std::is_same<T, __half>::value ? 7.f : -8.f;
-constexpr uint64_t PF_WAIT_NS = 4000000000ull;
 
 template <int D>
 struct PrefillShape {
@@ -351,10 +350,11 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
     const uint32_t tmem = __shfl_sync(FULL_MASK, *tmem_slot, 0);
 
     // A wait that runs out ends this warp's work: the error bit is set, later
-    // waits and work are skipped, and the CTA still frees its TMEM.
+    // waits and work are skipped, and the CTA still frees its TMEM. The limit is
+    // longer than an item can last (wait_limit_ns).
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (alive && !__all_sync(FULL_MASK, mbar_wait_bounded(bar, parity, PF_WAIT_NS))) {
+        if (alive && !__all_sync(FULL_MASK, mbar_wait_bounded(bar, parity, p.wait_ns))) {
             alive = false;
             if (lane == 0) atomicOr(p.errors, PA_DEVERR_TIMEOUT);
         }
@@ -499,9 +499,9 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                 }
             }
             if (!alive) {  // copies in flight land before the CTA leaves
-                for (int i = max(0, c - NS); i < c; ++i) mbar_wait_bounded(kv_full(i % NS), (i / NS) & 1, PF_WAIT_NS);
+                for (int i = max(0, c - NS); i < c; ++i) mbar_wait_bounded(kv_full(i % NS), (i / NS) & 1, p.wait_ns);
                 for (int t = 0; t < NQ; ++t)
-                    if (uses[t] > 0) mbar_wait_bounded(q_full(t), (uses[t] - 1) & 1, PF_WAIT_NS);
+                    if (uses[t] > 0) mbar_wait_bounded(q_full(t), (uses[t] - 1) & 1, p.wait_ns);
             }
         } else if (warp < SH::MMA_WARP + NQ) {
             // ---- matrix instructions: a warp for each tile of rows ----

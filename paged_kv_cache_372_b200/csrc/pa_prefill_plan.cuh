@@ -27,6 +27,7 @@ struct PrefillParams {
     int part_slots;    // places for parts of a chain
     float *part_acc;   // [slot][row of the chain][head_dim]: weighted values of the parts
     float2 *part_ml;   // [slot][row of the chain]: what they are relative to (log2), sum of the weights
+    unsigned long long wait_ns;  // after which a wait gives up
     unsigned int *errors;
 };
 

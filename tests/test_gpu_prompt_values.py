@@ -100,3 +100,32 @@ def test_sums_of_values_near_the_largest_of_bf16(n, rows):
     assert (out == 2.0 ** 120).all()
     if n == rows:
         assert (run_packed(q, k, v, [0, n], 0.1, compare=False) == 2.0 ** 120).all()
+
+
+def long_row(n):
+    """Seconds and the result of one row over n keys in the row form, a warp's work, while the 8 warps' next work item
+    waits: the last of 56 sequences is long, and one of its 8 heads has scores of 2^30."""
+    H, D, bs, B = 8, 64, 64, 56
+    width = -(-n // bs)
+    q, kp, vp = (normal(s, torch.float16, gen(83)) for s in ((B, H, D), (3, H, bs, D), (3, H, bs, D)))
+    q[-1, 0] = 8192.0
+    kp[:2, 0] = 8192.0
+    kp[1, 0, 0] *= 1.25  # the key that takes all of the weight
+    table = torch.zeros((B, width), dtype=torch.int32, device="cuda")
+    table[:-1, 0] = 2
+    table[-1, width // 2] = 1
+    out = torch.full_like(q, 7.0)
+    args = (out, q, kp, vp, table, ints([1] * (B - 1) + [n]), ints(list(range(B + 1))), 0.125, n)
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ends[0].record()
+    pa.pa_prefill_paged(*args)
+    ends[1].record()
+    assert pa.pa_device_errors() == 0
+    assert torch.equal(bits(out[-1, 0]), bits(vp[1, 0, 0]))
+    assert torch.equal(bits(out[:-1]), bits(vp[2, :, 0].expand(B - 1, H, D)))
+    return ends[0].elapsed_time(ends[1]) / 1e3
+
+
+def test_an_item_may_last_longer_than_a_wait():
+    # a wait of 4 seconds would have run out
+    assert long_row(50_000_000) > 4.2
