@@ -520,7 +520,9 @@ PA_API pa_status pa_rope_and_cache(void *q_out, void *k_out, const void *q, cons
  * [0, num_tokens]; other values are clamped and flagged (PA_DEVERR_TOKENS).
  * Rows outside every sequence are left as they were. A row's result depends on
  * the rows it sees only: infinities and NaN in later rows, in other sequences
- * and behind the last one do not reach it.
+ * and behind the last one do not reach it. A tile of rows that comes out other
+ * than finite is computed twice (a prompt of them takes 2 to 3 times as long);
+ * rows with scores of 2^22 and more take 100 ns a key each.
  * q, k, v and their strides as in pa_rope_and_cache; out [num_tokens][num_heads]
  * [head_dim] contiguous, not overlapping an input. Heads, head_dim and
  * dtype as pa_decode; fewer than 2^27 tokens. scale must be finite (at most 2^127

@@ -1,10 +1,24 @@
 // Device side of the prompt attention (pa_prefill, pa_prefill_paged;
-// include/pa.h): the row-at-a-time form.
+// include/pa.h): the row-at-a-time form, for rows of very large scores, and
+// values that are not finite.
 #pragma once
 
 #include "pa_prefill_plan.cuh"
 
 namespace pa {
+
+// Row j of sequence s in the keys or values x.
+template <int D, typename T, bool PAGED>
+__device__ __forceinline__ const T *kv_row(const PrefillParams &p, const void *x, long long stride, int s, int row0,
+                                           int kvh, int j) {
+    if constexpr (PAGED) {
+        int id = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / p.block_size];
+        if ((unsigned)id >= (unsigned)p.num_blocks) id = 0;  // flagged where the tile was loaded
+        return static_cast<const T *>(x) + (((size_t)id * p.num_kv_heads + kvh) * p.block_size + j % p.block_size) * D;
+    } else {
+        return static_cast<const T *>(x) + (size_t)(row0 + j) * stride + (size_t)kvh * D;
+    }
+}
 
 // What a row has from a range of keys: weighted values relative to the maximum
 // m (log2 units) and the sum of the weights; D / 32 elements a lane.
@@ -22,14 +36,7 @@ __device__ __noinline__ RowPart<D> attend_row(const PrefillParams &p, int s, int
     const int lane = threadIdx.x & 31;
     const int kvh = h / (p.num_heads / p.num_kv_heads);
     auto base = [&](const void *x, long long stride, int j) {
-        if constexpr (PAGED) {
-            int id = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / p.block_size];
-            if ((unsigned)id >= (unsigned)p.num_blocks) id = 0;  // flagged where the tile was loaded
-            return static_cast<const T *>(x) +
-                   (((size_t)id * p.num_kv_heads + kvh) * p.block_size + j % p.block_size) * D;
-        } else {
-            return static_cast<const T *>(x) + (size_t)(row0 + j) * stride + (size_t)kvh * D;
-        }
+        return kv_row<D, T, PAGED>(p, x, stride, s, row0, kvh, j);
     };
     const uint32_t *qp =
         reinterpret_cast<const uint32_t *>(static_cast<const T *>(p.q) + (size_t)row * p.q_stride + (size_t)h * D);
@@ -82,6 +89,71 @@ __device__ __noinline__ RowPart<D> attend_row(const PrefillParams &p, int s, int
         }
     }
     return r;
+}
+
+// Puts back the values that are not finite among the keys [from, to) of a KV head, which the products took as 0: the sum
+// of those that a row sees is added to its stored result (PART: part, else output), a lane a row of the warp (seen: its
+// visible keys, at most to; at: its row in the results). What a weight above 0 makes of an infinity or a NaN does not
+// depend on the weight; where the key is not finite either, the weight may be 0 and the result is NaN.
+template <int D, typename T, bool PAGED, bool PART>
+__device__ __noinline__ void add_bad_values(const PrefillParams &p, int s, int row0, int kvh, int from, int to, int seen,
+                                            size_t at) {
+    constexpr int E = D / 32, AHEAD = 8;  // keys loaded at a time
+    const int lane = threadIdx.x & 31;
+    auto words = [&](const void *x, long long stride, int j) {  // this lane's elements of row j
+        return reinterpret_cast<const uint32_t *>(kv_row<D, T, PAGED>(p, x, stride, s, row0, kvh, j)) + lane * (E / 2);
+    };
+    auto fine = [](float x) { return fabsf(x) < INFINITY; };
+    float sum[E] = {};
+    for (int j0 = from; j0 < to; j0 += AHEAD) {
+        uint32_t v[AHEAD][E / 2];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) v[i][e] = words(p.v, p.v_stride, min(j0 + i, to - 1))[e];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int j = j0 + i;
+            if (j >= to) break;
+            bool bad = false;
+            float add[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float2 x = Elem<T>::pair(v[i][e / 2]);
+                add[e] = e % 2 ? x.y : x.x;
+                bad = bad || !fine(add[e]);
+            }
+            if (__any_sync(FULL_MASK, bad)) {
+                bool bad_key = false;
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    const float2 x = Elem<T>::pair(words(p.k, p.k_stride, j)[e]);
+                    bad_key = bad_key || !fine(x.x) || !fine(x.y);
+                }
+                bad_key = __any_sync(FULL_MASK, bad_key);
+#pragma unroll
+                for (int e = 0; e < E; ++e) sum[e] += fine(add[e]) ? 0.f : bad_key ? NAN : add[e];
+            }
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e) any = any || !fine(sum[e]);
+            if (!__any_sync(FULL_MASK, any)) continue;
+            for (unsigned rows = __ballot_sync(FULL_MASK, seen == j + 1); rows; rows &= rows - 1) {
+                const size_t row = __shfl_sync(FULL_MASK, at, __ffs(rows) - 1);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (fine(sum[e])) continue;
+                    if constexpr (PART) {
+                        p.part_acc[row * D + lane * E + e] += sum[e];
+                    } else {
+                        T &o = static_cast<T *>(p.out)[row * D + lane * E + e];
+                        o = T((float)o + sum[e]);
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
 }
 
 // Stores a part of a split context as row `at` of the parts.

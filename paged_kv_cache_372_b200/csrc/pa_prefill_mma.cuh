@@ -35,10 +35,14 @@
 // over 4096-32768 tokens: 91 us, 5.3 TB/s of the cache.
 //
 // Masked places: S is replaced by -inf there (a selection, so NaN and
-// infinities in masked keys do not spread) and P is 0. A NaN or infinity in a
-// masked value row would still come through 0 x V: such a row of O is NaN, is
-// seen at the end, and is computed again by the row form (attend_row), which
-// reads the visible rows only.
+// infinities in masked keys do not spread) and P is 0. Value rows that no row of an
+// item sees are made 0. A NaN or infinity in another masked value row still comes
+// through 0 x V. So an item with a row that is not finite is walked again: this time
+// the copying warp looks through the value rows that are hidden from some row (at
+// most 256, at the diagonal) when they have landed, and makes what is not finite 0
+// there (clear_bad); at the item's end it is added to the results of the rows that
+// see it (add_bad_values). Looked through in every item, by whichever warps, they
+// cost 2 to 6% of a call. A row whose scores are NaN or infinite is NaN as it is.
 #pragma once
 
 #include <cuda.h>
@@ -60,6 +64,10 @@ constexpr int PF_POLY = D == 64 ? 4 : 5;
 // range or ex2_fma's. Rows whose maximum has been past this size are computed again by the row form, which
 // subtracts the maximum from the scaled scores.
 constexpr float PF_COARSE = 4194304.f;  // 2^22
+// What an item's warps say of it: a row is not finite, it has to be walked again; values were made 0.
+constexpr uint32_t PF_AGAIN = 1, PF_CLEARED = 2;
+// Sums of weights are below this: 2^30 keys of 2^15. From here on one of them was NaN.
+constexpr float PF_SOUND = 1152921504606846976.f;  // 2^60
 // Weights are lifted to where the type has room. fp16: by 2^7, so that the largest
 // (2^15 and the factor above) is just below 65504 and rounding is to 2^-32 of the
 // largest, not 2^-25: long contexts of small weights add up. bf16, whose range has
@@ -83,10 +91,11 @@ struct PrefillShape {
     static constexpr int S_COL = 0, O_COL = PF_NQ * 128;
     static constexpr int OFF_KV = PF_NQ * TILE;
     static constexpr int OFF_NEXT = OFF_KV + STAGES * TILE;  // 16 bytes: the launch taken over
-    static constexpr int OFF_ITEM = OFF_NEXT + 16;           // the work item, 10 integers
+    static constexpr int OFF_ITEM = OFF_NEXT + 16;           // the work item, 11 integers
     static constexpr int OFF_TMEM = OFF_ITEM + 48;           // TMEM address
+    static constexpr int OFF_NOTE = OFF_TMEM + 4;            // of an item and the next: PF_AGAIN, PF_CLEARED
     static constexpr int OFF_BAR = OFF_TMEM + 16;
-    static constexpr int NUM_BARS = 2 * STAGES + 5 + 6 * PF_NQ;
+    static constexpr int NUM_BARS = 2 * STAGES + 6 + 6 * PF_NQ;
     static constexpr int OFF_SWAP = OFF_BAR + (NUM_BARS + 1) / 2 * 16;  // the second tile's maxima and sums
     static constexpr int BYTES = OFF_SWAP + PF_BM * 8 + 1024;           // and slack for the alignment to 1024
 };
@@ -193,6 +202,48 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r) {
         : "memory");
 }
 
+__device__ __forceinline__ uint32_t load_shared(uint32_t at) {
+    uint32_t x;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+
+// A set bit 15 or 31 for each half that is NaN or infinite: a full exponent carries into the sign's place.
+template <typename T>
+__device__ __forceinline__ uint32_t bad_halves(uint32_t x) {
+    constexpr uint32_t MASK = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    constexpr uint32_t ONE = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+    return (x & MASK) + ONE & 0x80008000u;
+}
+
+__device__ __forceinline__ uint4 load_shared_16(uint32_t at) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+    return x;
+}
+
+// Makes what is NaN or infinite 0 in the value rows [from, to) of a stage, by one warp, and says so before in the word
+// at `note`. GROUP, HALF: bytes from 8 rows to the next 8, and from one 64-element column to the next.
+template <int D, typename T, uint32_t GROUP, uint32_t HALF>
+__device__ __forceinline__ void clear_bad(uint32_t stage, int from, int to, uint32_t note) {
+    constexpr int VECTORS = D / 8;  // of a row
+    for (int i = from * VECTORS + (threadIdx.x & 31); i < to * VECTORS; i += 32) {
+        const int row = i / VECTORS, col = i % VECTORS;
+        const uint32_t at = stage + (row >> 3) * GROUP + (col >> 3) * HALF + (row & 7) * 128 + (col & 7) * 16;
+        const uint4 x = load_shared_16(at);
+        const uint32_t bx = bad_halves<T>(x.x), by = bad_halves<T>(x.y), bz = bad_halves<T>(x.z), bw = bad_halves<T>(x.w);
+        if (bx | by | bz | bw) {
+            auto good = [](uint32_t x, uint32_t bad) { return x & ~((bad >> 15) * 0xffffu); };
+            asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(note), "r"(PF_CLEARED) : "memory");
+            asm volatile("st.volatile.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(good(x.x, bx)),
+                         "r"(good(x.y, by)), "r"(good(x.z, bz)), "r"(good(x.w, bw))
+                         : "memory");
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 // ---- tensor-map copies --------------------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
@@ -259,7 +310,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // [-1/2, 1/2] with the constant term 1 (a linear programme over 4001 points):
 // 1.0e-4 of degree 3 for bf16, whose weights are rounded to 2^-9, 2.9e-6 of degree
 // 4 for fp16. x below -127 counts as -127, whose f is 0 and whose result is 0.
-// x up to 16; a NaN gives a weight so large that the row's sums overflow.
+// x up to 16; a NaN gives a weight near 2^128, past any that a sum of others reaches (PF_SOUND).
 template <typename T>
 __device__ __forceinline__ float2 ex2_fma(float2 x) {
     x.x = max_nan(x.x, -127.f);
@@ -292,6 +343,9 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
     pa_prefill_mma_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ PrefillMaps maps) {
     using SH = PrefillShape<D>;
     constexpr int HALVES = SH::HALVES, NS = SH::STAGES, NQ = PF_NQ;
+    // Keys and values: rows of 128 bytes in groups of 8 (1024 bytes), for the
+    // packed form column after column, for the pools' chunks row group after row group.
+    constexpr uint32_t KV_GROUP = PAGED ? HALVES * 1024 : 1024, KV_HALF = PAGED ? 1024 : 16384;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     const uint32_t base = smem_u32(smem);
@@ -299,8 +353,8 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
     auto kv_full = [&](int i) { return bars + 8 * i; };
     auto kv_empty = [&](int i) { return bars + 8 * (NS + i); };
     const uint32_t item_full = bars + 8 * (2 * NS), item_empty = item_full + 8, next_full = item_full + 16,
-                   pair_full = item_full + 24, pair_empty = item_full + 32;
-    auto stream_bar = [&](int k, int t) { return bars + 8 * (2 * NS + 5 + k * NQ + t); };
+                   pair_full = item_full + 24, pair_empty = item_full + 32, look_full = item_full + 40;
+    auto stream_bar = [&](int k, int t) { return bars + 8 * (2 * NS + 6 + k * NQ + t); };
     auto q_full = [&](int t) { return stream_bar(0, t); };
     auto q_empty = [&](int t) { return stream_bar(1, t); };
     auto s_full = [&](int t) { return stream_bar(2, t); };
@@ -324,6 +378,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             mbar_init(next_full, 1);
             mbar_init(pair_full, 4);
             mbar_init(pair_empty, 4);
+            mbar_init(look_full, 1);
             for (int t = 0; t < NQ; ++t) {
                 mbar_init(q_full(t), 1);
                 mbar_init(q_empty(t), 1);
@@ -374,6 +429,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
         it.kvh = __shfl_sync(FULL_MASK, at[7], 0);
         it.j0 = __shfl_sync(FULL_MASK, at[8], 0);
         it.j1 = __shfl_sync(FULL_MASK, at[9], 0);
+        it.look = __shfl_sync(FULL_MASK, at[10], 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(item_empty);
         return it.s >= 0;
@@ -384,16 +440,59 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
         if (warp == SH::PLAN_WARP) {
             // ---- finds the work items ----
             Finder<PAGED> finder;
-            int index = blockIdx.x;
+            const bool deal = PAGED && p.deal;
             unsigned bad = 0;
+            int launches = 0;   // asked for
+            bool more = true;   // there may be further items
+            auto find_next = [&](Item &it) {
+                if (deal) return finder.next_piece(p, NQ * tm, it, bad);
+                int index = blockIdx.x;
+                if (launches > 0) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(next_full, 16);
+                        asm volatile(
+                            "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                            ::"r"(base + SH::OFF_NEXT), "r"(next_full)
+                            : "memory");
+                    }
+                    __syncwarp();
+                    if (!wait(next_full, (launches - 1) & 1)) return false;
+                    uint32_t taken, x;
+                    asm volatile(
+                        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+                        "ld.shared.b128 r, [%2];\n\t"
+                        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+                        : "=r"(taken), "=r"(x)
+                        : "r"(base + SH::OFF_NEXT)
+                        : "memory");
+                    fence_proxy_async_smem();  // read before it is written again
+                    index = __shfl_sync(FULL_MASK, taken ? (int)x : -1, 0);
+                }
+                ++launches;
+                return index >= 0 && finder.find(p, index, NQ * tm, it, bad);
+            };
+            // Items go out one ahead of the softmax warps. When all warps have one, the softmax warps are done with
+            // the one before, and what they say of it holds: it goes out again, or the next one does. Behind the last
+            // an empty item (no rows) waits for what they say of that.
+            Item last{}, before{};
             for (int nth = 0;; ++nth) {
-                Item it;
-                const bool deal = PAGED && p.deal;
-                const bool work = deal ? finder.next_piece(p, NQ * tm, it, bad)
-                                       : index >= 0 && finder.find(p, index, NQ * tm, it, bad);
-                if (!work) it.s = -1;
+                Item it{};
+                it.parts = 1;
+                const uint32_t note = base + SH::OFF_NOTE + (nth & 1) * 4;
+                if (nth >= 2 && __shfl_sync(FULL_MASK, load_shared(note), 0) == PF_AGAIN) {
+                    it = before;
+                    it.look = 1;
+                } else if (more && (more = find_next(it))) {
+                    it.look = 0;
+                } else if (nth == 0 || last.n == 0 || last.look) {
+                    it.s = -1;
+                }
                 if (nth == 0 && __any_sync(FULL_MASK, bad != 0) && bad) atomicOr(p.errors, bad);
+                __syncwarp();
                 if (lane == 0) {
+                    tmem_slot[1 + (nth & 1)] = 0;
                     int *at = reinterpret_cast<int *>(smem + SH::OFF_ITEM);
                     at[0] = it.s;
                     at[1] = it.tok0;
@@ -405,39 +504,18 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                     at[7] = it.kvh;
                     at[8] = it.j0;
                     at[9] = it.j1;
+                    at[10] = it.look;
                     mbar_arrive(item_full);
                 }
                 __syncwarp();
-                if (!work) break;
-                // When every warp has this item, the next launch is taken over.
-                if (!wait(item_empty, nth & 1)) break;
-                if (deal) continue;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(next_full, 16);
-                    asm volatile(
-                        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
-                        ::"r"(base + SH::OFF_NEXT), "r"(next_full)
-                        : "memory");
-                }
-                __syncwarp();
-                if (!wait(next_full, nth & 1)) break;
-                uint32_t taken, x;
-                asm volatile(
-                    "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
-                    "ld.shared.b128 r, [%2];\n\t"
-                    "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-                    "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-                    "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
-                    : "=r"(taken), "=r"(x)
-                    : "r"(base + SH::OFF_NEXT)
-                    : "memory");
-                fence_proxy_async_smem();  // read before it is written again
-                index = __shfl_sync(FULL_MASK, taken ? (int)x : -1, 0);
+                if (it.s < 0 || !wait(item_empty, nth & 1)) break;
+                before = last;
+                last = it;
             }
         } else if (warp == SH::COPY_WARP) {
             // ---- copies ----
             Item it;
-            int c = 0, uses[NQ] = {};  // chunks (key or value tiles) issued; query tiles
+            int c = 0, uses[NQ] = {}, looks = 0;  // chunks (key or value tiles) issued; query tiles; chunks looked through
             for (int nth = 0; alive && next_item(nth, it); ++nth) {
                 const Walk w = walk_of(it, tm, PAGED);
                 auto queries = [&](int t) {
@@ -465,41 +543,63 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                     }
                     return id;
                 };
-                int id_next = 0;
-                if constexpr (PAGED) id_next = block_of(w.j0);
-                for (int j = w.j0; j < w.j1 && alive; ++j) {
-                    const int id = id_next;
-                    if constexpr (PAGED) {
-                        if (j + 1 < w.j1) id_next = block_of(j + 1);
-                    }
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const int stage = c % NS;
-                        if (c >= NS && !wait(kv_empty(stage), (c / NS - 1) & 1)) break;
-                        const CUtensorMap *map = kv ? &maps.v : &maps.k;
-                        const uint32_t dst = base + SH::OFF_KV + stage * SH::TILE;
+                const int hidden = w.first + it.tok0 + 1;  // keys from here on are hidden from some row
+                // Two forms of the loop: the tests for the rare one in the other's code cost 2 to 5% of a call.
+                auto copy_tiles = [&](auto looking) {
+                    constexpr bool LOOK = decltype(looking)::value;
+                    int id_next = 0;
+                    if constexpr (PAGED) id_next = block_of(w.j0);
+                    for (int j = w.j0; j < w.j1 && alive; ++j) {
+                        [[maybe_unused]] const int id = id_next;
                         if constexpr (PAGED) {
-                            const int chunk = p.block_size * D * 2;
-                            const int blocks = min(per_tile, (w.kv_end - j * PF_BN + p.block_size - 1) / p.block_size);
-                            if (lane == 0) mbar_arrive_expect_tx(kv_full(stage), blocks * chunk);
-                            __syncwarp();
-                            if (lane < blocks)
-                                tma_load_chunk(dst + lane * chunk, map, id * p.num_kv_heads + it.kvh, kv_full(stage));
-                        } else if (lane == 0) {
-                            mbar_arrive_expect_tx(kv_full(stage), SH::TILE);
-                            for (int h = 0; h < HALVES; ++h)
-                                tma_load_3d(dst + h * 16384, map, h * 64, it.kvh, it.row0 + j * PF_BN, kv_full(stage));
+                            if (j + 1 < w.j1) id_next = block_of(j + 1);
                         }
-                        __syncwarp();
-                        ++c;
-                        // The second tile of rows still multiplies the last item's keys: its
-                        // queries come behind the first keys.
-                        if (kv == 0 && j == w.j0) queries(1);
+#pragma unroll
+                        for (int kv = 0; kv < 2; ++kv) {
+                            const int stage = c % NS;
+                            if (c >= NS && !wait(kv_empty(stage), (c / NS - 1) & 1)) break;
+                            const CUtensorMap *map = kv ? &maps.v : &maps.k;
+                            const uint32_t dst = base + SH::OFF_KV + stage * SH::TILE;
+                            const bool look = LOOK && kv && (j + 1) * PF_BN > hidden;
+                            const uint32_t full = look ? look_full : kv_full(stage);
+                            if constexpr (PAGED) {
+                                const int chunk = p.block_size * D * 2;
+                                const int blocks = min(per_tile, (w.kv_end - j * PF_BN + p.block_size - 1) / p.block_size);
+                                if (lane == 0) mbar_arrive_expect_tx(full, blocks * chunk);
+                                __syncwarp();
+                                if (lane < blocks)
+                                    tma_load_chunk(dst + lane * chunk, map, id * p.num_kv_heads + it.kvh, full);
+                            } else if (lane == 0) {
+                                mbar_arrive_expect_tx(full, SH::TILE);
+                                for (int h = 0; h < HALVES; ++h)
+                                    tma_load_3d(dst + h * 16384, map, h * 64, it.kvh, it.row0 + j * PF_BN, full);
+                            }
+                            if constexpr (LOOK) {
+                                if (look) {
+                                    ++looks;
+                                    if (!wait(look_full, (looks - 1) & 1)) break;
+                                    clear_bad<D, T, KV_GROUP, KV_HALF>(dst, max(hidden - j * PF_BN, 0),
+                                                                       min(w.kv_end - j * PF_BN, PF_BN),
+                                                                       base + SH::OFF_NOTE + (nth & 1) * 4);
+                                    if (lane == 0) mbar_arrive(kv_full(stage));
+                                }
+                            }
+                            __syncwarp();
+                            ++c;
+                            // The second tile of rows still multiplies the last item's keys: its
+                            // queries come behind the first keys.
+                            if (kv == 0 && j == w.j0) queries(1);
+                        }
                     }
-                }
+                };
+                if (it.look)
+                    copy_tiles(std::true_type());
+                else
+                    copy_tiles(std::false_type());
             }
             if (!alive) {  // copies in flight land before the CTA leaves
                 for (int i = max(0, c - NS); i < c; ++i) mbar_wait_bounded(kv_full(i % NS), (i / NS) & 1, p.wait_ns);
+                if (looks > 0) mbar_wait_bounded(look_full, (looks - 1) & 1, p.wait_ns);
                 for (int t = 0; t < NQ; ++t)
                     if (uses[t] > 0) mbar_wait_bounded(q_full(t), (uses[t] - 1) & 1, p.wait_ns);
             }
@@ -512,9 +612,6 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
             constexpr uint32_t common = 1u << 4 | type << 7 | type << 10 | (uint32_t)(PF_BM >> 4) << 24;
             const uint32_t idesc_qk = common | (p.negate ? 1u << 13 : 0u);  // and N
             constexpr uint32_t idesc_pv = common | (uint32_t)(D >> 3) << 17 | 1u << 16;
-            // Keys and values: rows of 128 bytes in groups of 8 (1024 bytes), for the
-            // packed form column after column, for the pools' chunks row group after row group.
-            constexpr uint32_t KV_GROUP = PAGED ? HALVES * 1024 : 1024, KV_HALF = PAGED ? 1024 : 16384;
             const uint32_t one = elect_one();
             const int t = warp - SH::MMA_WARP;
             const uint32_t s_at = uniform(tmem + SH::S_COL + t * 128), o_at = uniform(tmem + SH::O_COL + t * D);
@@ -528,12 +625,13 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                 tc_commit(s_full(t), one);
             };
             int weights = 0;  // tiles of weights taken
-            // The product with the values in a stage; there: keys of the tile below kv_end.
+            // The product with the values in a stage; there: keys of the tile below kv_end, cols: those multiplied.
             auto pv = [&](int stage, int there, int cols, bool add) {
                 const uint32_t v = base + SH::OFF_KV + stage * SH::TILE, vd = desc_lo(v, KV_HALF);
-                if (PAGED && there < PF_BN) {
-                    // Slots behind the context hold anything: their weights are 0, their values made 0.
-                    for (int i = there * HALVES * 8 + lane; i < PF_BN * HALVES * 8; i += 32) {
+                if (there < cols) {
+                    // Value rows behind all that is seen (slots behind the context, the next sequence's
+                    // rows) hold anything: their weights are 0, their values made 0.
+                    for (int i = there * HALVES * 8 + lane; i < cols * HALVES * 8; i += 32) {
                         const int row = i / (HALVES * 8), col = i % (HALVES * 8);
                         const uint32_t at = v + (row >> 3) * KV_GROUP + (col >> 3) * KV_HALF + (row & 7) * 128 + (col & 7) * 16;
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
@@ -679,7 +777,7 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                     const float f = grow ? ex2((m - top) * p.scale_log2) : 1.f;
                     m = grow ? top : m;
                     coarse = coarse || (fabsf(m) * p.scale_log2 >= PF_COARSE && fabsf(m) < INFINITY);
-                    l *= f;
+                    l = l < PF_SOUND ? l * f : NAN;
                     if (j > 0) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
@@ -750,15 +848,18 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                 const float top = fmaxf(m, other.x);
                 f0 = m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
                 f1 = other.x == -INFINITY ? 0.f : ex2((other.x - top) * p.scale_log2);
-                l = l * f0 + other.y * f1;
+                l = (l < PF_SOUND ? l : NAN) * f0 + (other.y < PF_SOUND ? other.y : NAN) * f1;
                 m = top;
             }
+            // Else a score is NaN or +inf, or none is above -inf: the row is NaN.
+            const bool sound = l > 0.f && l < PF_SOUND;
             if (it.parts == 1) {
-                const float inv = 1.f / l;
+                const float inv = sound ? 1.f / l : NAN;
                 f0 *= inv;
                 f1 *= inv;
+            } else if (!(l < PF_SOUND)) {
+                l = NAN;
             }
-            bool again = some && (coarse || !(l > 0.f && l < INFINITY));
             if (mine > 0) {
                 if (!wait(o_full(t), (t == 0 ? results0 : results1) & 1)) break;
                 tc_fence_after();
@@ -826,12 +927,24 @@ __global__ void __launch_bounds__(PrefillShape<D>::THREADS, 1)
                     for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0, 0, 0, 0);
                 }
             }
-            const float2 any = add2(add2(nan[0], nan[1]), add2(nan[2], nan[3]));
-            again = again || (some && !(any.x + any.y == 0.f));
             tc_fence_before();
             __syncwarp();
             if (w.halves && lane == 0) mbar_arrive(pair_empty);
-            for (unsigned rows = __ballot_sync(FULL_MASK, again); rows; rows &= rows - 1) {
+            const float2 any = add2(add2(nan[0], nan[1]), add2(nan[2], nan[3]));
+            const uint32_t note = base + SH::OFF_NOTE + (nth & 1) * 4;
+            // Not finite, though the weights are (in a part they may all be 0).
+            const bool unsure = some && !coarse && !(any.x + any.y == 0.f) && (it.parts == 1 ? sound : l < PF_SOUND);
+            if (!it.look) {
+                if (__any_sync(FULL_MASK, unsure) && lane == 0)
+                    asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(note), "r"(PF_AGAIN) : "memory");
+            } else if (__any_sync(FULL_MASK, load_shared(note) == PF_CLEARED)) {
+                const int from = max(w.first + it.tok0 + 1, lo), to = min(w.kv_end, w.j1 * PF_BN);
+                if (PAGED && it.parts > 1)
+                    add_bad_values<D, T, PAGED, true>(p, it.s, it.row0, it.kvh, from, to, hi, part_at);
+                else
+                    add_bad_values<D, T, PAGED, false>(p, it.s, it.row0, it.kvh, from, to, hi, at);
+            }
+            for (unsigned rows = __ballot_sync(FULL_MASK, some && coarse); rows; rows &= rows - 1) {
                 const int src = __ffs(rows) - 1;
                 const int row = it.row0 + __shfl_sync(FULL_MASK, tok, src), h = __shfl_sync(FULL_MASK, head, src);
                 const RowPart<D> part =

@@ -57,6 +57,7 @@ struct Item {
     int row0, n, keys;     // as SeqRange
     int slot, parts, kvh;  // the part's place, how many parts the chain has, KV head
     int j0, j1;            // key tiles of the part, where there are more than one
+    int look;              // whether hidden values are looked through
 };
 
 // Key tiles an item walks, [j0, j1), and how its two tiles of rows share them:

@@ -129,3 +129,152 @@ def long_row(n):
 def test_an_item_may_last_longer_than_a_wait():
     # a wait of 4 seconds would have run out
     assert long_row(50_000_000) > 4.2
+
+
+def milliseconds(call):
+    for _ in range(2):
+        call()
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ends[0].record()
+    call()
+    ends[1].record()
+    torch.cuda.synchronize()
+    assert pa.pa_device_errors() == 0
+    return ends[0].elapsed_time(ends[1])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("where", ["first key", "first value", "all values", "behind the last"])
+def test_one_bad_row_does_not_slow_the_others(bad, where):
+    # a row alone, key by key, takes 100 ns a key: 8190 rows of 8 heads in that form took 400 times the whole call
+    n, tail = 8190, 50
+    q, k, v = (normal((n + tail, h, 128), torch.bfloat16, gen(84)) for h in (8, 2, 2))
+    out, cu = torch.empty_like(q), ints([0, n])
+    clean = milliseconds(lambda: pa.pa_prefill(out, q, k, v, cu, 0.088))
+    want = out.clone()
+    if where == "first key":
+        k[0, :, 5] = bad
+    elif where == "first value":
+        v[0, :, 5] = bad
+    elif where == "all values":
+        v[:, :, 5] = float("nan")
+    else:
+        k[n:], v[n:], q[n:] = bad, bad, bad
+    took = milliseconds(lambda: pa.pa_prefill(out, q, k, v, cu, 0.088))
+    assert took < 5 * clean + 0.5, f"{took:.2f} ms against {clean:.2f}"
+    if where == "behind the last":
+        assert torch.equal(bits(out[:n]), bits(want[:n]))
+    elif where == "first key":
+        assert torch.isnan(out[:n]).all() if bad != bad else True
+    else:
+        assert not torch.isfinite(out[:n, :, 5]).any()
+        others = torch.arange(128, device="cuda") != 5
+        assert torch.equal(bits(out[:n, :, others]), bits(want[:n, :, others]))
+
+
+def formula(q, k, v, scale, first):
+    """ref.attention where values that are not finite count for the rows that see them only."""
+    want, bound = ref.attention(q, k, v.where(torch.isfinite(v), 0.0), scale, first)
+    n, H, D = q.shape
+    for j, h, d in (~torch.isfinite(v)).nonzero().tolist():
+        heads = slice(h * H // v.shape[1], (h + 1) * H // v.shape[1])
+        z = torch.einsum("ngd,d->ng", q[max(j - first, 0):, heads].double(), k[j, h].double()) * scale
+        # weight 0 (a score of -inf) times infinity is NaN
+        want[max(j - first, 0):, heads, d] += torch.where(z == -float("inf"), float("nan"), v[j, h, d].double())
+    return want, bound
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_bad_values_anywhere(seed):
+    """NaN, infinities and values half of the type's largest at random places of keys and values: what the formula gives, row by row."""
+    g = torch.Generator().manual_seed(300 + seed)
+
+    def pick(*x):
+        return x[int(torch.randint(0, len(x), (1,), generator=g))]
+
+    Hkv, group, D, bs = pick(1, 2), pick(1, 2, 4, 8), pick(64, 128), pick(16, 64)
+    dtype = pick(torch.float16, torch.bfloat16)
+    H, n = Hkv * group, pick(150, 700, 1500)
+    rows = n if seed % 2 else pick(3, 40)
+    q, k, v = (normal((n, h, D), dtype, gen(300 + seed)) for h in (H, Hkv, Hkv))
+    for x, kinds in ((k, [float("nan"), float("inf"), -float("inf")]),
+                     (v, [float("nan"), float("inf"), -float("inf"), torch.finfo(dtype).max / 2])):
+        for _ in range(pick(0, 1, 3, 20)):
+            j = int(torch.randint(0, n, (1,), generator=g)) if pick(0, 1) else n - 1 - int(torch.randint(0, 140, (1,), generator=g))
+            x[j, pick(*range(Hkv)), int(torch.randint(0, D, (1,), generator=g))] = pick(*kinds)
+    want, bound = formula(q[n - rows:], k, v, 0.09, n - rows)
+    outs = []
+    if rows == n:
+        outs.append(run_packed(q, k, v, [0, n], 0.09, compare=False))
+    kp, vp, table = one_pool(k, v, bs)
+    out = torch.full((rows, H, D), 7.0, dtype=dtype, device="cuda")
+    pa.pa_prefill_paged(out, q[n - rows:], kp, vp, table, ints([n]), ints([0, rows]), 0.09, n)
+    assert pa.pa_device_errors() == 0
+    for out in outs + [out]:
+        fine = torch.isfinite(want)
+        assert torch.isnan(out[torch.isnan(want)]).all()
+        assert not torch.isfinite(out[~fine]).any()
+        err = (out.double() - want).abs()
+        assert (err <= bound)[fine].all()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("Hkv,group,D,dtype", [(2, 1, 128, torch.float16), (1, 4, 128, torch.bfloat16),
+                                               (2, 8, 64, torch.bfloat16)])
+def test_bad_values_in_some_of_many_sequences(paged, Hkv, group, D, dtype):
+    """Several work items for each SM, some walked twice: the other sequences' rows keep their bits."""
+    g = torch.Generator().manual_seed(Hkv + group)
+    lens = torch.randint(0, 500, (150,), generator=g).tolist() + [2500, 1, 0, 900]
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    T, H = cu[-1], Hkv * group
+    q, k, v = (normal((T + 9, h, D), dtype, gen(310)) for h in (H, Hkv, Hkv))
+    v[T:] = float("nan")
+    if paged:
+        bs = 32
+        width = -(-max(lens) // bs)
+        used = [-(-n // bs) for n in lens]
+        table = torch.full((len(lens), width), -3, dtype=torch.int32)
+        first = 0
+        for s, w in enumerate(used):
+            table[s, :w] = torch.arange(first, first + w)
+            first += w
+        table = table.cuda()
+
+    def run(v):
+        out = torch.full_like(q, 7.0)
+        if not paged:
+            pa.pa_prefill(out, q, k, v, ints(cu), 0.09)
+        else:
+            pools = []
+            for x in (k, v):
+                rows = torch.full((first * bs, Hkv, D), float("nan"), dtype=dtype, device="cuda")
+                at = 0
+                for s, w in enumerate(used):
+                    rows[at:at + lens[s]] = x[cu[s]:cu[s + 1]]
+                    at += w * bs
+                pools.append(rows.view(first, bs, Hkv, D).transpose(1, 2).contiguous())
+            pa.pa_prefill_paged(out, q, *pools, table, ints(lens), ints(cu), 0.09, max(lens))
+        assert pa.pa_device_errors() == 0
+        assert (out[T:] == 7.0).all()
+        return out
+
+    clean = run(v)
+    bad = v.clone()
+    hurt = [s for s in range(0, len(lens), 7) if lens[s]] + [150, 153]
+    for s in hurt:
+        for kind in (float("nan"), float("inf"), -float("inf")):
+            j = cu[s] + int(torch.randint(0, lens[s], (1,), generator=g))
+            bad[j, int(torch.randint(0, Hkv, (1,), generator=g)), int(torch.randint(0, D, (1,), generator=g))] = kind
+    out = run(bad)
+    for s in range(len(lens)):
+        a, b = cu[s], cu[s + 1]
+        if s not in hurt:
+            assert torch.equal(bits(out[a:b]), bits(clean[a:b]))
+        elif b > a:
+            want, bound = formula(q[a:b], k[a:b], bad[a:b], 0.09, 0)
+            fine = torch.isfinite(want)
+            assert torch.isnan(out[a:b][torch.isnan(want)]).all()
+            assert not torch.isfinite(out[a:b][~fine]).any()
+            assert torch.equal(out[a:b][fine], clean[a:b][fine])
