@@ -633,7 +633,16 @@ def _rows(t, name, shape, dtype, dev) -> int:
     st, sh, se = t.stride()
     if se != 1 or (h > 1 and sh != D):
         raise ValueError(f"{name}: a token's heads and elements must be contiguous")
-    return st if T > 1 else h * D
+    if T <= 1:
+        return h * D
+    if st >= 1 << 31:  # the C ABI takes 32 bits, and ctypes would drop the others
+        raise ValueError(f"{name}: tokens are {st} elements apart (fewer than 2^31 are supported)")
+    return st
+
+
+def _context_limit(n) -> None:
+    if n >= 1 << 31:
+        raise ValueError(f"max_context_len {n} (at most 2^30 - 1 is supported)")
 
 
 def _heads(q, name="q"):
@@ -748,6 +757,7 @@ def pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_head
                                     max_context_len) -> int:
     """Workspace bytes for pa_prefill_paged on the current device: enough for calls with at most these num_seqs,
     num_tokens and max_context_len."""
+    _context_limit(max_context_len)
     n = int(lib().pa_prefill_paged_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size,
                                                   max_context_len))
     if n == 0:
@@ -780,6 +790,7 @@ def pa_prefill_paged(out, q, k_pool, v_pool, block_tables, context_lens, cu_seql
     NB, Hkv, bs, _ = k_pool.shape
     pool = (NB, Hkv, bs, D)
     B, W = tables = block_tables.shape
+    _context_limit(max_context_len)
     if workspace is None:
         workspace = _scratch(alloc_prefill_workspace, stream, dev, B, T, H, Hkv, D, bs, max_context_len, dev)
     elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():

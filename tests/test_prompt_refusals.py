@@ -132,3 +132,19 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
     with pytest.raises(ValueError):
         pa.pa_assign_slots(tab, torch.zeros(3, dtype=i32), ctx, torch.zeros(1, dtype=i32), ctx, 16,
                            torch.zeros(4, dtype=i64), torch.zeros(4, dtype=i32), cu)
+
+
+def test_binding_refuses_numbers_past_32_bits():
+    # a view of every second token of a very wide buffer: no memory behind it here
+    def rows(step):
+        x = torch.empty_strided((2, 8, 64), (step, 64, 1), dtype=torch.float16, device="meta")
+        return pa._rows(x, "q", x.shape, torch.float16, x.get_device())
+
+    assert rows((1 << 31) - 8) == (1 << 31) - 8
+    for step in (1 << 31, (1 << 32) + 512):
+        with pytest.raises(ValueError, match="apart"):
+            rows(step)
+    with pytest.raises(ValueError, match="max_context_len"):
+        pa.pa_prefill_paged_workspace_size(4, 64, 8, 2, 128, 16, (1 << 32) + 128)
+    for n in (1 << 30, (1 << 31) - 1):
+        assert paged(max_ctx=n) == pa.PA_ERR_UNSUPPORTED
