@@ -43,13 +43,18 @@ pa_status encode_pool(PFN_cuTensorMapEncodeTiled enc, CUtensorMap *map, CUtensor
 
 constexpr int kMaxDevices = 64;
 
-// Contexts are split where there are fewer items than kSplitItems an SM (a paged
-// call of few rows), unless they are shorter than two parts of 4 key tiles. The
-// device deals their key tiles to the SMs in equal shares. Not split, 512-token
-// pieces of eight 32768-token prompts (3.5 items an SM) take 1969 us back to back, in
-// two parts each 1998.
-constexpr long long kSplitItems = 3;
-constexpr int kSplitLeast = 8;  // key tiles of the longest context, at least
+// Contexts are split where there are so few items that half of the SMs would have
+// none, the contexts are at least kSplitLeast key tiles long, and there are at most
+// kSplitRows rows (token, query head) for each key of the longest: every row's parts
+// are written, read and joined. Split / not split in us, 32/8 heads of 128, contexts
+// of equal length, tokens each (items an SM, rows a key):
+//   1 x 32768: 8 tokens (0.05, 1/128) 37 / 267, 512 (0.43, 1/2) 257 / 370, 1024 (0.86, 1) 509 / 409
+//   1 x 4096: 8 (0.05, 1/16) 17 / 38, 128 (0.11, 1) 35 / 55, 256 (0.22, 2) 57 / 55, 512 (0.43, 4) 87 / 57
+//   8 x 32768: 8 (0.43, 1/16) 179 / 337; 16 x 32768: 8 (0.86, 1/8) 343 / 342
+//   1 x 1024: 8 (0.05, 1/4) 17 / 17, 128 (0.11, 4) 33 / 22; whole prompt of 2048: 212 / 53
+// The device deals the key tiles to the SMs in equal shares. It counts those that a
+// mask hides, so a prompt's first chunk is dealt unevenly.
+constexpr int kSplitLeast = 16, kSplitRows = 2;
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -139,7 +144,8 @@ bool splits(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int m
     const long long items = std::max<long long>(std::min(num_seqs, num_tokens),
                                                 ceil_div(num_tokens, item_tokens(num_heads, num_kv_heads))) *
                             num_kv_heads;
-    return items < kSplitItems * sms && ceil_div(max_keys, pa::PF_BN) >= kSplitLeast;
+    return 2 * items <= sms && ceil_div(max_keys, pa::PF_BN) >= kSplitLeast &&
+           (long long)num_tokens * num_heads <= (long long)kSplitRows * max_keys;
 }
 
 // Places for the parts of a split call: struct Deal. Each has room for an item's rows.
@@ -235,10 +241,10 @@ size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_hea
     if (num_seqs == 0 || num_tokens == 0) return 256;
     int dev, sms;
     if (pa_internal_device(&dev, &sms) != PA_OK) return 0;
-    // Enough for every call that is no larger: one that splits has at most kSplitItems an SM
-    // of full items, and as many that are not full.
+    // Enough for every call that is no larger: one that splits has at most half an SM's
+    // number of full items, and as many that are not full.
     if (ceil_div(max_context_len, pa::PF_BN) < kSplitLeast) return 256;
-    const long long most = (2 * kSplitItems + 1) * sms;
+    const long long most = 2 * sms;
     return parts_bytes(std::min(part_slots(num_seqs, num_tokens, num_heads, num_kv_heads, sms), most), head_dim);
 }
 

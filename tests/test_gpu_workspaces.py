@@ -87,3 +87,31 @@ def test_a_workspace_too_small_for_its_call_is_refused():
     with pytest.raises(pa.PagedAttentionError) as e:
         pa.pa_prefill_paged(out, q, kp, vp, table, ints(ctx), ints(cu), 0.1, 3000, ws[:n - 256])
     assert e.value.status == pa.PA_ERR_INVALID and (out == 7.0).all()
+
+
+def microseconds(call):
+    for _ in range(3):
+        call()
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ends[0].record()
+    for _ in range(20):
+        call()
+    ends[1].record()
+    torch.cuda.synchronize()
+    return ends[0].elapsed_time(ends[1]) * 50
+
+
+@pytest.mark.parametrize("n,limit", [(2048, 2048), (3500, 3500), (2048, 32768)])
+def test_a_whole_prompt_over_the_cache_takes_about_the_packed_call(n, limit):
+    # split among the SMs it took four times as long
+    H, Hkv, D, bs = 32, 8, 128, 16
+    q, kp, vp, table, cu = pooled([n], [n], H, Hkv, D, bs, torch.bfloat16, 72)
+    wide = torch.zeros((1, limit // bs + 1), dtype=torch.int32, device="cuda")
+    wide[:, :min(table.shape[1], wide.shape[1])] = table[:, :wide.shape[1]]
+    ctx, cu = ints([n]), ints(cu)
+    out, ws = torch.empty_like(q), pa.alloc_prefill_workspace(1, q.shape[0], H, Hkv, D, bs, limit)
+    k, v = torch.randn((2, q.shape[0], Hkv, D), device="cuda").to(q.dtype)
+    paged = microseconds(lambda: pa.pa_prefill_paged(out, q, kp, vp, wide, ctx, cu, 0.09, limit, ws))
+    whole = microseconds(lambda: pa.pa_prefill(out, q, k, v, cu, 0.09))
+    assert pa.pa_device_errors() == 0
+    assert paged < 2 * whole, f"{paged:.0f} us against {whole:.0f}"
