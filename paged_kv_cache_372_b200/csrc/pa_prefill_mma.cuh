@@ -29,10 +29,10 @@
 // clocks, 2,048 of them products: the chain of a tile of rows (scores 512, to
 // registers 150, maximum 300, exponentials 1,200, hand-over twice 200, last
 // quarter of the product 128) is what remains, and two chains are all that the
-// 512 columns of TMEM hold. 16384 tokens, 32/8 heads, bf16: 1.50 ms after a pause
-// (1,467 TFLOP/s at 1.8 GHz), 1.77 ms back to back, where 1,000 W hold the clock
-// at 1.45 GHz. The tensor pipe is active 75% of the time. 5-8 tokens of 8 requests
-// over 4096-32768 tokens: 91 us, 5.3 TB/s of the cache.
+// 512 columns of TMEM hold. 16384 tokens, 32/8 heads, bf16: 1.53 ms after a pause
+// (1,437 TFLOP/s at 1.8 GHz), 1.78 ms back to back, where 1,000 W hold the clock
+// at 1.45 GHz. The tensor pipe is active 73% of the time. 5-8 tokens of 8 requests
+// over 4096-32768 tokens: 92 us, 5.3 TB/s of the cache.
 //
 // Masked places: S is replaced by -inf there (a selection, so NaN and
 // infinities in masked keys do not spread) and P is 0. Value rows that no row of an
