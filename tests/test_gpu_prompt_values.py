@@ -278,3 +278,30 @@ def test_bad_values_in_some_of_many_sequences(paged, Hkv, group, D, dtype):
             assert torch.isnan(out[a:b][torch.isnan(want)]).all()
             assert not torch.isfinite(out[a:b][~fine]).any()
             assert torch.equal(out[a:b][fine], clean[a:b][fine])
+
+
+@pytest.mark.parametrize("rows", [1, 3, 40, 100])
+@pytest.mark.parametrize("Hkv,group,D,bs,dtype", [(1, 1, 64, 16, torch.float16), (2, 4, 128, 32, torch.bfloat16),
+                                                  (1, 8, 128, 64, torch.float16)])
+def test_bad_values_in_split_contexts(rows, Hkv, group, D, bs, dtype):
+    """Parts of a chain, walked in halves where the rows are few: bad rows at the diagonal, in other parts, at a part's edge."""
+    n, H = 5000, Hkv * group
+    g = torch.Generator().manual_seed(rows + group)
+    q, k, v = (normal((m, h, D), dtype, gen(320 + rows)) for m, h in ((rows, H), (n, Hkv), (n, Hkv)))
+    assert pa.pa_prefill_paged_workspace_size(1, rows, H, Hkv, D, bs, n) > 256
+    places = [0, 127, 128, 2559, 2560, n - 1, n - rows, n - 1 - rows // 2, n - 1 - rows // 3]
+    for i, j in enumerate(places):
+        kind = (float("nan"), float("inf"), -float("inf"))[i % 3]
+        d = int(torch.randint(0, D, (1,), generator=g))
+        v[j, i % Hkv, d] = kind
+        if i % 4 == 3:
+            k[j, i % Hkv, (d + 1) % D] = -float("inf")
+    kp, vp, table = one_pool(k, v, bs)
+    out = torch.full((rows, H, D), 7.0, dtype=dtype, device="cuda")
+    pa.pa_prefill_paged(out, q, kp, vp, table, ints([n]), ints([0, rows]), 0.09, n)
+    assert pa.pa_device_errors() == 0
+    want, bound = formula(q, k, v, 0.09, n - rows)
+    fine = torch.isfinite(want)
+    assert torch.isnan(out[torch.isnan(want)]).all()
+    assert not torch.isfinite(out[~fine]).any()
+    assert ((out.double() - want).abs() <= bound)[fine].all()
