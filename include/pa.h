@@ -546,7 +546,7 @@ PA_API pa_status pa_prefill(void *out, const void *q, const void *k, const void 
  * as pa_prefill. Cache slots past a context are never read into a result.
  * max_context_len is below 2^30, num_blocks * num_kv_heads below 2^31.
  *
- * Where the rows are too few to fill half of the device, and few beside
+ * Where the rows are too few to fill the device, and few beside
  * max_context_len, their contexts are split and the parts merged by the
  * log-sum-exp identity in a second launch. A max_context_len far above the
  * contexts can make a call split that is faster whole.
@@ -565,8 +565,8 @@ PA_API pa_status pa_prefill_paged(void *out, const void *q, const void *k_pool, 
 
 /* Workspace bytes that suffice for pa_prefill_paged with at most these
  * num_seqs, num_tokens and max_context_len on the current device (0 if the shape
- * is invalid). It grows with each of them, up to 2 parts an SM: 40 MB at
- * head_dim 128, 20 MB at 64 on 148 SMs. */
+ * is invalid). It grows with each of them, up to 5 parts an SM: 99 MB at
+ * head_dim 128, 50 MB at 64 on 148 SMs. */
 PA_API size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
                                               int head_dim, int block_size, int max_context_len);
 

@@ -43,18 +43,23 @@ pa_status encode_pool(PFN_cuTensorMapEncodeTiled enc, CUtensorMap *map, CUtensor
 
 constexpr int kMaxDevices = 64;
 
-// Contexts are split where there are so few items that half of the SMs would have
-// none, the contexts are at least kSplitLeast key tiles long, and there are at most
-// kSplitRows rows (token, query head) for each key of the longest: every row's parts
-// are written, read and joined. Split / not split in us, 32/8 heads of 128, contexts
-// of equal length, tokens each (items an SM, rows a key):
-//   1 x 32768: 8 tokens (0.05, 1/128) 37 / 267, 512 (0.43, 1/2) 257 / 370, 1024 (0.86, 1) 509 / 409
-//   1 x 4096: 8 (0.05, 1/16) 17 / 38, 128 (0.11, 1) 35 / 55, 256 (0.22, 2) 57 / 55, 512 (0.43, 4) 87 / 57
-//   8 x 32768: 8 (0.43, 1/16) 179 / 337; 16 x 32768: 8 (0.86, 1/8) 343 / 342
-//   1 x 1024: 8 (0.05, 1/4) 17 / 17, 128 (0.11, 4) 33 / 22; whole prompt of 2048: 212 / 53
-// The device deals the key tiles to the SMs in equal shares. It counts those that a
-// mask hides, so a prompt's first chunk is dealt unevenly.
-constexpr int kSplitLeast = 16, kSplitRows = 2;
+// Contexts of at least kSplitLeast key tiles are split below kSplitItems items an SM,
+// where the longest item may be more than an SM's share, if the rows (token, query
+// head) are few: each row's parts are written, read and joined, 3 ns a row, and a key
+// tile is 1.4 us of one SM's time, so a third of a row a key tile is 10% more time. Where
+// half of the SMs would have no item, up to kSplitRows rows a key of the longest.
+// Split / not split in us, 32/8 heads of 128, tokens each (items an SM):
+//   contexts of equal length
+//   1 x 32768: 8 tokens (0.05) 37 / 267, 512 (0.43) 257 / 370, 1024 (0.86) 509 / 409 *
+//   1 x 4096: 8 (0.05) 17 / 38, 128 (0.11) 35 / 55, 256 (0.22) 57 / 55, 512 (0.43) 87 / 57 *
+//   16 x 32768 (0.86): 8 343 / 342, 32 404 / 336 *; whole prompt of 2048 (1.7) 212 / 53 *
+//   contexts of 4096-32768
+//   8 (0.43): 8 82 / 210; 16 (0.86): 8 199 / 263; 36 (1.95): 8 421 / 464; 48 (2.6): 8 571 / 565 *
+//   contexts of 512-4096
+//   8 (0.43): 8 27 / 35; 16 (0.86): 1 39 / 42, 16 60 / 43 *
+// (*: the rule does not split). The device deals the key tiles to the SMs in equal
+// shares. It counts those that a mask hides, so a prompt's first chunk is dealt unevenly.
+constexpr int kSplitLeast = 16, kSplitRows = 2, kSplitItems = 2;
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -144,8 +149,9 @@ bool splits(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int m
     const long long items = std::max<long long>(std::min(num_seqs, num_tokens),
                                                 ceil_div(num_tokens, item_tokens(num_heads, num_kv_heads))) *
                             num_kv_heads;
-    return 2 * items <= sms && ceil_div(max_keys, pa::PF_BN) >= kSplitLeast &&
-           (long long)num_tokens * num_heads <= (long long)kSplitRows * max_keys;
+    const long long tiles = ceil_div(max_keys, pa::PF_BN), rows = (long long)num_tokens * num_heads;
+    if (items >= kSplitItems * sms || tiles < kSplitLeast) return false;
+    return 3 * rows <= items * tiles || (2 * items <= sms && rows <= (long long)kSplitRows * max_keys);
 }
 
 // Places for the parts of a split call: struct Deal. Each has room for an item's rows.
@@ -241,10 +247,10 @@ size_t pa_prefill_paged_workspace_size(int num_seqs, int num_tokens, int num_hea
     if (num_seqs == 0 || num_tokens == 0) return 256;
     int dev, sms;
     if (pa_internal_device(&dev, &sms) != PA_OK) return 0;
-    // Enough for every call that is no larger: one that splits has at most half an SM's
-    // number of full items, and as many that are not full.
+    // Enough for every call that is no larger: one that splits has fewer than kSplitItems
+    // full items an SM, and as many that are not full.
     if (ceil_div(max_context_len, pa::PF_BN) < kSplitLeast) return 256;
-    const long long most = 2 * sms;
+    const long long most = (2 * kSplitItems + 1) * sms;
     return parts_bytes(std::min(part_slots(num_seqs, num_tokens, num_heads, num_kv_heads, sms), most), head_dim);
 }
 

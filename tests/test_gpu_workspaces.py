@@ -115,3 +115,16 @@ def test_a_whole_prompt_over_the_cache_takes_about_the_packed_call(n, limit):
     whole = microseconds(lambda: pa.pa_prefill(out, q, k, v, cu, 0.09))
     assert pa.pa_device_errors() == 0
     assert paged < 2 * whole, f"{paged:.0f} us against {whole:.0f}"
+
+
+def test_a_few_tokens_over_unequal_contexts_take_no_longer_than_their_cache():
+    # 16 requests over 4096 to 32768 tokens: whole, the longest of them took the SMs that have it 263 us; split 199
+    H, Hkv, D, bs, B, n = 32, 8, 128, 64, 16, 8
+    ctx = [4096 + 28672 * i // (B - 1) for i in range(B)]
+    q, kp, vp, table, cu = pooled(ctx, [n] * B, H, Hkv, D, bs, torch.bfloat16, 73)
+    ctx_d, cu = ints(ctx), ints(cu)
+    out, ws = torch.empty_like(q), pa.alloc_prefill_workspace(B, q.shape[0], H, Hkv, D, bs, max(ctx))
+    took = microseconds(lambda: pa.pa_prefill_paged(out, q, kp, vp, table, ctx_d, cu, 0.09, max(ctx), ws))
+    assert pa.pa_device_errors() == 0
+    bytes_read = 2 * 2 * D * Hkv * sum(ctx)
+    assert took < 1.2 * bytes_read / 6.0e6 + 20, f"{took:.0f} us for {bytes_read / 1e6:.0f} MB"
